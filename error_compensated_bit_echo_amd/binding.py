@@ -1,4 +1,4 @@
-"""Thin Python binding of libecho (include/echo.h).
+"""Thin Python binding of libecho (include/echo.h, include/echo_layer.h).
 
 Argument marshalling only: every step of the pipeline runs in the HIP
 kernels of libecho.so.  PyTorch provides device memory and streams: tensors
@@ -44,6 +44,12 @@ class EchoConfigC(C.Structure):
                 ("alpha_slow", C.c_float), ("max_elements", C.c_int64)]
 
 
+class EchoNormDescC(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("hidden", C.c_int64), ("ld_y", C.c_int64), ("ld_h", C.c_int64),
+                ("gate_rows", C.c_int64), ("dtype", C.c_int32), ("stream_dtype", C.c_int32),
+                ("post", C.c_int32), ("pre", C.c_int32), ("scale", C.c_float), ("eps", C.c_float)]
+
+
 _vp = C.c_void_p
 _pp = C.POINTER(C.c_void_p)
 _SIGNATURES = {
@@ -70,17 +76,25 @@ _SIGNATURES = {
     "echo_status_string": [C.c_int],
     "echo_version": [],
 }
+# include/echo_layer.h: the layer operators beside the all-reduce
+_LAYER_SIGNATURES = {
+    "echo_norm": [C.POINTER(EchoNormDescC)] + [_vp] * 11,
+    "echo_norm_backward_workspace": [C.POINTER(EchoNormDescC)],
+    "echo_norm_backward": [C.POINTER(EchoNormDescC)] + [_vp] * 17 + [C.c_int64, _vp],
+}
+_RETURNS = {"echo_status_string": C.c_char_p, "echo_norm_backward_workspace": C.c_int64}
 EXPORTED = tuple(_SIGNATURES)
+EXPORTED_LAYER = tuple(_LAYER_SIGNATURES)
 
 
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libecho.so not built at {LIB_PATH}; run __graft_entry__.build()")
     lib = C.CDLL(LIB_PATH)
-    for name, args in _SIGNATURES.items():
+    for name, args in {**_SIGNATURES, **_LAYER_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.argtypes = args
-        fn.restype = C.c_char_p if name == "echo_status_string" else C.c_int
+        fn.restype = _RETURNS.get(name, C.c_int)
     return lib
 
 
@@ -383,6 +397,140 @@ def echo_call_prepare(st: EchoState, x, recv_codes, recv_scales, gath_codes, gat
     """A reusable echo_call on fixed buffers (see PreparedCall)."""
     return PreparedCall(st, x, recv_codes, recv_scales, gath_codes, gath_scales, send_codes,
                         send_scales, own_codes2, own_scales2, y)
+
+
+# ---- layer operators: norms and products beside the all-reduce -------------------
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _code(table, key, what):
+    if key not in table:
+        raise ValueError(f"{what}: {key!r} is not one of {', '.join(map(str, table))}")
+    return table[key]
+
+
+def _tensor(t, dtype, what):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: a tensor is required")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: a GPU tensor is required (got one on {t.device})")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: {dtype} is required (got {t.dtype})")
+
+
+def _matrix(t, rows, cols, dtype, what):
+    """(address, row pitch in elements) of a [rows, cols] matrix with unit
+    stride along its rows, or of a dense tensor of any shape whose last
+    dimension is cols."""
+    _tensor(t, dtype, what)
+    if t.dim() == 0 or t.shape[-1] != cols or t.numel() != rows * cols:
+        raise ValueError(f"{what}: shape {tuple(t.shape)} does not hold {rows} rows of {cols}")
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{what}: rows of unit stride that do not overlap are required "
+                         f"(strides {t.stride()})")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _dense(t, shape, dtype, what):
+    """address of a dense tensor of as many elements as `shape` has (None -> NULL)"""
+    if t is None:
+        return None
+    _tensor(t, dtype, what)
+    n = 1
+    for s in shape:
+        n *= s
+    if t.numel() != n or (len(shape) > 1 and n and t.shape[-1] != shape[-1]):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: the tensor must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace(t):
+    """(address, bytes) of a workspace tensor (None -> NULL, 0)"""
+    if t is None:
+        return None, 0
+    return _ptr(t, 0, "workspace"), t.nbytes
+
+
+def _rows_of(t, what):
+    if not isinstance(t, torch.Tensor) or t.dim() == 0 or t.dtype not in DTYPES:
+        raise ValueError(f"{what}: a bfloat16, float16 or float32 tensor with rows is required")
+    cols = t.shape[-1]
+    return (t.numel() // cols if cols else 0), cols
+
+
+def _same_pitch(a, b, what):
+    if a is not None and b is not None and a != b:
+        raise ValueError(f"{what}: the same row pitch is required (got {a} and {b})")
+    return a if a is not None else (b if b is not None else 0)
+
+
+def echo_norm(h, y, h_out, z, *, post="none", w_post=None, b_post=None, gate=None, scale=1.0,
+              pre="rms", w_pre=None, b_pre=None, eps=1e-6, stats=None, stream=None) -> None:
+    """h_out = h + scale * gate * N_post(y); z = N_pre(h_out), row by row.
+
+    h and h_out [tokens, hidden] in the stream's type, y and z in y's type (or
+    the stream's own); gate [rows, hidden] with tokens a multiple of its rows;
+    weights and biases [hidden]; stats float32 [4, tokens] where a backward
+    pass follows.  post and pre are "none", "rms" or "layer".  y, h_out and z
+    may be None as include/echo_layer.h says; h_out may be h."""
+    T, H = _rows_of(h, "h")
+    first = next((t for t in (y, z, w_pre) if t is not None), h)
+    if not isinstance(first, torch.Tensor) or first.dtype not in DTYPES:
+        raise ValueError("y, z: a bfloat16, float16 or float32 tensor is required")
+    dt, sdt = first.dtype, h.dtype
+    hp, ldh = _matrix(h, T, H, sdt, "h")
+    yp, ldy = _matrix(y, T, H, dt, "y") if y is not None else (None, 0)
+    op, ldo = _matrix(h_out, T, H, sdt, "h_out") if h_out is not None else (None, None)
+    G = 0 if gate is None else _rows_of(gate, "gate")[0]
+    d = EchoNormDescC(T, H, ldy, _same_pitch(ldh, ldo, "h, h_out"), G, DTYPES[dt], DTYPES[sdt],
+                      _code(NORMS, post, "post"), _code(NORMS, pre, "pre"), float(scale), float(eps))
+    _check(lib.echo_norm(C.byref(d), hp, yp, _dense(gate, (G, H), dt, "gate"),
+                         _dense(w_post, (H,), dt, "w_post"), _dense(b_post, (H,), dt, "b_post"),
+                         _dense(w_pre, (H,), dt, "w_pre"), _dense(b_pre, (H,), dt, "b_pre"), op,
+                         _dense(z, (T, H), dt, "z"), _dense(stats, (4, T), torch.float32, "stats"),
+                         _stream(stream)), "echo_norm")
+
+
+def echo_norm_backward_workspace(tokens, hidden, gate_rows=0) -> int:
+    """bytes of workspace echo_norm_backward takes for this shape"""
+    d = EchoNormDescC(int(tokens), int(hidden), 0, 0, int(gate_rows), 0, 0, 0, 0, 1.0, 0.0)
+    n = lib.echo_norm_backward_workspace(C.byref(d))
+    _check(min(n, 0), "echo_norm_backward_workspace")
+    return n
+
+
+def echo_norm_backward(dz, dh_out, h_out, y, stats, dh, dy, *, post="none", w_post=None, b_post=None,
+                       gate=None, scale=1.0, pre="rms", w_pre=None, dw_post=None, db_post=None,
+                       dgate=None, dw_pre=None, db_pre=None, workspace=None, stream=None) -> None:
+    """Gradients of echo_norm: dh (may be dh_out), dy, and the parameters'
+    gradients that are given, from dz and dh_out with the forward call's y,
+    h_out and stats.  The parameters are those of the forward call; workspace
+    is needed where a parameter's gradient is wanted."""
+    T, H = _rows_of(dh, "dh")
+    first = next((t for t in (dz, dy, y) if t is not None), dh)
+    if not isinstance(first, torch.Tensor) or first.dtype not in DTYPES:
+        raise ValueError("dz, dy, y: a bfloat16, float16 or float32 tensor is required")
+    dt, sdt = first.dtype, dh.dtype
+    hp, ldh = _matrix(h_out, T, H, sdt, "h_out") if h_out is not None else (None, 0)
+    yp, ldy = _matrix(y, T, H, dt, "y") if y is not None else (None, 0)
+    G = 0 if gate is None else _rows_of(gate, "gate")[0]
+    d = EchoNormDescC(T, H, ldy, ldh, G, DTYPES[dt], DTYPES[sdt], _code(NORMS, post, "post"),
+                      _code(NORMS, pre, "pre"), float(scale), 0.0)
+    vec = lambda t, what: _dense(t, (H,), dt, what)  # noqa: E731
+    wp, wn = _workspace(workspace)
+    _check(lib.echo_norm_backward(
+        C.byref(d), _dense(dz, (T, H), dt, "dz"), _dense(dh_out, (T, H), sdt, "dh_out"), hp, yp,
+        _dense(stats, (4, T), torch.float32, "stats"), _dense(gate, (G, H), dt, "gate"),
+        vec(w_post, "w_post"), vec(b_post, "b_post"), vec(w_pre, "w_pre"),
+        _dense(dh, (T, H), sdt, "dh"), _dense(dy, (T, H), dt, "dy"), _dense(dgate, (G, H), dt, "dgate"),
+        vec(dw_post, "dw_post"), vec(db_post, "db_post"), vec(dw_pre, "dw_pre"), vec(db_pre, "db_pre"),
+        wp, wn, _stream(stream)), "echo_norm_backward")
 
 
 def echo_get_config() -> dict:

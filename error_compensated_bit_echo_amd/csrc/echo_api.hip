@@ -11,6 +11,7 @@
 
 #include "echo.h"
 #include "echo_device.h"
+#include "host_checks.h"
 
 using namespace echo;
 
@@ -42,31 +43,10 @@ constexpr int kU1 = ECHO_U_STAGE1;  // stage-1 slices (2 groups each) per wave s
 constexpr int kUR = ECHO_U_REDUCE;  // reduce slices per wave step
 constexpr int kUD = ECHO_U_EXIT;    // exit: quads of groups per wave step
 
-// Launch `kernel` with its one by-value argument struct.  The status is the
-// launch's own (hipLaunchKernel's return value), so an error an earlier,
-// unrelated HIP call left in the thread's last-error slot is neither
-// reported as this call's nor cleared.
-template <typename A>
-int launch(void (*kernel)(A), dim3 grid, hipStream_t s, A arg) {
-  void* argv[] = {&arg};
-  const hipError_t e =
-      hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kBlock), argv, 0, s);
-  return e == hipSuccess ? ECHO_SUCCESS : ECHO_ERR_HIP;
-}
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
 bool bits_ok(int32_t bits) { return bits == 4 || bits == 8; }
 
 // bytes of the codes of n elements: packed nibbles, or one byte per code
 int64_t code_bytes(int64_t n, int32_t bits) { return bits == 8 ? n : n / 2; }
-
-// A check that passed with nothing to do: zero elements.  The entry point
-// then returns ECHO_SUCCESS without looking at its pointers or launching.
-constexpr int kEmpty = 1;
-
-// the status an entry point returns for a check result that is not SUCCESS
-int finished(int rc) { return rc < 0 ? rc : ECHO_SUCCESS; }
 
 int check_elements(int64_t n, int64_t multiple) {
   if (n < 0 || n > ECHO_MAX_ELEMENTS || n % multiple != 0) return ECHO_ERR_SHAPE;
@@ -89,45 +69,6 @@ int check_state(const echo_state* st) {
   if (!aligned(st->m_fast, 16) || !aligned(st->m_slow, 16)) return ECHO_ERR_ALIGNMENT;
   return ECHO_SUCCESS;
 }
-
-// Byte ranges written (outputs, including read-modify-write state) and read
-// (inputs).  Outputs must be pairwise disjoint and disjoint from every
-// input, except one explicitly allowed identical pair (y == x in place).
-class Aliases {
- public:
-  void out(const void* p, int64_t bytes) { add(outs_, no_, p, bytes); }
-  void in(const void* p, int64_t bytes) { add(ins_, ni_, p, bytes); }
-  void allow_identical(const void* a, const void* b) { allow_a_ = a; allow_b_ = b; }
-  bool ok() const {
-    for (int i = 0; i < no_; ++i) {
-      for (int j = i + 1; j < no_; ++j)
-        if (overlap(outs_[i], outs_[j])) return false;
-      for (int j = 0; j < ni_; ++j)
-        if (overlap(outs_[i], ins_[j]) && !allowed(outs_[i], ins_[j])) return false;
-    }
-    return true;
-  }
-
- private:
-  struct Span { uintptr_t lo, hi; };
-  static constexpr int kCap = 4 * ECHO_MAX_RANKS + 16;
-  static void add(Span* s, int& k, const void* p, int64_t bytes) {
-    if (!p || bytes <= 0 || k >= kCap) return;
-    s[k].lo = (uintptr_t)p;
-    s[k].hi = (uintptr_t)p + (uintptr_t)bytes;
-    ++k;
-  }
-  static bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
-  bool allowed(const Span& o, const Span& i) const {
-    if (!allow_a_) return false;
-    const uintptr_t a = (uintptr_t)allow_a_, b = (uintptr_t)allow_b_;
-    return o.lo == i.lo && o.hi == i.hi && ((o.lo == a && i.lo == b) || (o.lo == b && i.lo == a));
-  }
-  Span outs_[kCap], ins_[kCap];
-  int no_ = 0, ni_ = 0;
-  const void* allow_a_ = nullptr;
-  const void* allow_b_ = nullptr;
-};
 
 #ifndef ECHO_UPDATE_MAX_BLOCKS
 #define ECHO_UPDATE_MAX_BLOCKS kMaxBlocks
@@ -834,6 +775,8 @@ const char* echo_status_string(int status) {
     case ECHO_ERR_HIP: return "HIP runtime error";
     case ECHO_ERR_ALIAS: return "outputs overlap each other or an input";
     case ECHO_ERR_FORMAT: return "code width must be 4 or 8 bits";
+    case ECHO_ERR_TYPE: return "unknown or unsupported element type, norm kind or activation";
+    case ECHO_ERR_WORKSPACE: return "workspace smaller than the call's workspace query says";
     default: return "unknown status";
   }
 }

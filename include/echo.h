@@ -107,6 +107,9 @@ extern "C" {
                                         nor cleared) */
 #define ECHO_ERR_ALIAS -6            /* outputs overlap each other or an input */
 #define ECHO_ERR_FORMAT -7           /* code width other than 4 or 8 bits */
+#define ECHO_ERR_TYPE -8             /* an element type, norm kind or activation that is
+                                        unknown or that the call does not take */
+#define ECHO_ERR_WORKSPACE -9        /* workspace_bytes below the call's query */
 
 typedef void* echo_stream_t; /* a hipStream_t */
 
