@@ -50,6 +50,12 @@ class EchoNormDescC(C.Structure):
                 ("post", C.c_int32), ("pre", C.c_int32), ("scale", C.c_float), ("eps", C.c_float)]
 
 
+class EchoLinearDescC(C.Structure):
+    _fields_ = [("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64), ("ld_x", C.c_int64),
+                ("ld_w", C.c_int64), ("ld_out", C.c_int64), ("ld_r", C.c_int64), ("dtype", C.c_int32),
+                ("act", C.c_int32), ("gated", C.c_int32), ("reserved", C.c_int32)]
+
+
 _vp = C.c_void_p
 _pp = C.POINTER(C.c_void_p)
 _SIGNATURES = {
@@ -81,8 +87,13 @@ _LAYER_SIGNATURES = {
     "echo_norm": [C.POINTER(EchoNormDescC)] + [_vp] * 11,
     "echo_norm_backward_workspace": [C.POINTER(EchoNormDescC)],
     "echo_norm_backward": [C.POINTER(EchoNormDescC)] + [_vp] * 17 + [C.c_int64, _vp],
+    "echo_linear_workspace": [C.POINTER(EchoLinearDescC)],
+    "echo_linear": [C.POINTER(EchoLinearDescC)] + [_vp] * 7 + [C.c_int64, _vp],
+    "echo_linear_backward_workspace": [C.POINTER(EchoLinearDescC)],
+    "echo_linear_backward": [C.POINTER(EchoLinearDescC)] + [_vp] * 8 + [C.c_int64, _vp],
 }
-_RETURNS = {"echo_status_string": C.c_char_p, "echo_norm_backward_workspace": C.c_int64}
+_RETURNS = {"echo_status_string": C.c_char_p, "echo_norm_backward_workspace": C.c_int64,
+            "echo_linear_workspace": C.c_int64, "echo_linear_backward_workspace": C.c_int64}
 EXPORTED = tuple(_SIGNATURES)
 EXPORTED_LAYER = tuple(_LAYER_SIGNATURES)
 
@@ -403,6 +414,7 @@ def echo_call_prepare(st: EchoState, x, recv_codes, recv_scales, gath_codes, gat
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 def _code(table, key, what):
@@ -531,6 +543,76 @@ def echo_norm_backward(dz, dh_out, h_out, y, stats, dh, dy, *, post="none", w_po
         _dense(dh, (T, H), sdt, "dh"), _dense(dy, (T, H), dt, "dy"), _dense(dgate, (G, H), dt, "dgate"),
         vec(dw_post, "dw_post"), vec(db_post, "db_post"), vec(dw_pre, "dw_pre"), vec(db_pre, "db_pre"),
         wp, wn, _stream(stream)), "echo_norm_backward")
+
+
+def _linear_desc(m, n, k, act, gated, dtype=0, ld_x=0, ld_w=0, ld_out=0, ld_r=0):
+    return EchoLinearDescC(int(m), int(n), int(k), ld_x, ld_w, ld_out, ld_r, dtype, _code(ACTS, act, "act"),
+                           1 if gated else 0, 0)
+
+
+def echo_linear_workspace(m, n, k, act="none", gated=False) -> int:
+    """bytes of workspace echo_linear takes for m rows of x, n outputs, k inputs"""
+    r = lib.echo_linear_workspace(C.byref(_linear_desc(m, n, k, act, gated)))
+    _check(min(r, 0), "echo_linear_workspace")
+    return r
+
+
+def echo_linear_backward_workspace(m, n, k, act="none", gated=False) -> int:
+    """bytes of workspace echo_linear_backward takes for this shape"""
+    r = lib.echo_linear_backward_workspace(C.byref(_linear_desc(m, n, k, act, gated)))
+    _check(min(r, 0), "echo_linear_backward_workspace")
+    return r
+
+
+def _linear_shape(x, w, gated):
+    m, k = _rows_of(x, "x") if x.shape[-1] else (x.numel() if x.dim() < 2 else x.shape[:-1].numel(), 0)
+    rows = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 2 else -1
+    if rows < 0 or (gated and rows % 2):
+        raise ValueError("w: a matrix is required, with an even number of rows if the product is gated")
+    return m, (rows // 2 if gated else rows), k, rows
+
+
+def echo_linear(x, w, out, *, bias=None, residual=None, act="none", gated=False, p=None, workspace=None,
+                stream=None) -> None:
+    """out = act(p) + residual for p = x w^T + bias; gated, w and bias hold the
+    gate's rows and then the up rows, and out = act(p_gate) * p_up + residual.
+
+    x [m, k], w [n, k] (gated [2n, k]), out and residual [m, n], bias and p
+    (dense, kept for the backward call) as wide as w has rows; all bfloat16 or
+    all float16.  act is "none", "relu", "gelu", "gelu_tanh" or "silu".  out may
+    be residual."""
+    if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("x: a bfloat16 or float16 tensor with rows is required")
+    m, n, k, rows = _linear_shape(x, w, gated)
+    dt = x.dtype
+    xp, ldx = _matrix(x, m, k, dt, "x")
+    wp, ldw = _matrix(w, rows, k, dt, "w")
+    op, ldo = _matrix(out, m, n, dt, "out")
+    rp, ldr = _matrix(residual, m, n, dt, "residual") if residual is not None else (None, 0)
+    d = _linear_desc(m, n, k, act, gated, DTYPES[dt], ldx, ldw, ldo, ldr)
+    sp, sn = _workspace(workspace)
+    _check(lib.echo_linear(C.byref(d), xp, wp, _dense(bias, (rows,), dt, "bias"), rp, op,
+                           _dense(p, (m, rows), dt, "p"), sp, sn, _stream(stream)), "echo_linear")
+
+
+def echo_linear_backward(dout, x, w, p, dx, dw, *, dbias=None, act="none", gated=False, workspace=None,
+                         stream=None) -> None:
+    """Gradients of echo_linear: dx, dw and dbias, each None to skip it, from
+    dout and the forward call's x, w and p (p may be None without an activation
+    and a gate).  The residual's gradient is dout."""
+    if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("x: a bfloat16 or float16 tensor with rows is required")
+    m, n, k, rows = _linear_shape(x, w, gated)
+    dt = x.dtype
+    gp, ldo = _matrix(dout, m, n, dt, "dout")
+    xp, ldx = _matrix(x, m, k, dt, "x")
+    wp, ldw = _matrix(w, rows, k, dt, "w")
+    d = _linear_desc(m, n, k, act, gated, DTYPES[dt], ldx, ldw, ldo, 0)
+    sp, sn = _workspace(workspace)
+    _check(lib.echo_linear_backward(C.byref(d), gp, xp, wp, _dense(p, (m, rows), dt, "p"),
+                                    _dense(dx, (m, k), dt, "dx"), _dense(dw, (rows, k), dt, "dw"),
+                                    _dense(dbias, (rows,), dt, "dbias"), sp, sn, _stream(stream)),
+           "echo_linear_backward")
 
 
 def echo_get_config() -> dict:

@@ -13,10 +13,12 @@ typedef _Float16 f16_t;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // The same 16 bytes at an address aligned to one element only: the global
 // load and store instructions of gfx950 take any alignment, so rows of odd
 // lengths need no second code path.
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
 __device__ __forceinline__ float to_f32(bf16_t v) { return __uint_as_float((uint32_t)v.bits << 16); }
@@ -118,6 +120,40 @@ __device__ __forceinline__ void store_n(T* p, int n, const float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) p[i] = from_f32<T>(f[i]);
+}
+
+// The same for W = 4 or 8 elements of a 16-bit type.
+template <typename T, int W>
+__device__ __forceinline__ void load_w(const T* p, int n, float (&f)[W]) {
+  if constexpr (W == 8) {
+    load_n<false>(p, n, f);
+  } else {
+    u32x2 w = {0, 0};
+    if (n >= 4) {
+      w = *reinterpret_cast<const u32x2_a2*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (i % 2 * 16);
+    }
+    float g[8];
+    unpack8(u32x4{w[0], w[1], 0, 0}, g, T{});
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = g[i];
+  }
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_w(T* p, int n, const float (&f)[W]) {
+  if constexpr (W == 8) {
+    store_n<false>(p, n, f);
+  } else if (n >= 4) {
+    const u32x2 w = {pack2(f[0], f[1], T{}), pack2(f[2], f[3], T{})};
+    *reinterpret_cast<u32x2_a2*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < n) p[i] = from_f32<T>(f[i]);
+  }
 }
 
 template <int CTRL>

@@ -1,0 +1,231 @@
+// linear_device.h -- gfx950 kernels of the matrix products with an epilogue.
+//
+// One kernel template covers the three products of a layer, each of the form
+// C[i][j] = sum over c of A(i, c) B(j, c):
+//   forward   out = x w^T     A = x  [m][k]    B = w [n][k]    c along the rows
+//   dx        dx  = dp w      A = dp [m][n]    B = w [n][k]^T  c across B's rows
+//   dw        dw  = dp^T x    A = dp [m][n]^T  B = x [m][k]^T  c across both
+// A workgroup computes a BI x BJ tile of C in steps of kC = 64 along c.  Both
+// operands' tiles are staged in LDS, two stages deep, and feed
+// v_mfma_f32_16x16x32: lane l of a wavefront holds, for row (or column) l % 16
+// of an operand's 16, the eight elements c = 8 (l / 16) .. + 7 of the 32.
+// B's fragment goes into the instruction's first operand, so a lane's four sums
+// are neighbours along j and the epilogue writes vectors along a row of C.
+//
+// LDS.  An operand whose rows run along c is stored row by row, 64 elements =
+// eight 16-byte chunks each, and a lane reads its eight elements with one
+// ds_read_b128.  An operand that c runs across is stored as it lies in memory,
+// 64 rows of c, and read with ds_read_b64_tr_b16: sixteen lanes read four rows
+// of sixteen elements and get them transposed.  Either way the chunks of a row
+// are permuted by an exclusive-or with bits of the row's number, so the lanes
+// of one read spread over the banks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "echo_layer.h"
+#include "layer_device.h"
+
+namespace echo {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kC = 64;  // contraction length of a step
+
+struct TileArgs {
+  const void *a, *b;
+  int64_t lda, ldb;
+  int64_t I, J, C;  // J counts outputs: gated, B has 2J rows
+  int64_t chunk;    // contraction length of one split, a multiple of kC
+  float* part;      // splits > 1: binary32 sums, [splits][I][columns of B]
+  void *out, *p;
+  const void *bias, *residual;
+  int64_t ldo, ldr;
+  uint32_t tiles_i, tiles_j, splits;
+  int32_t act;
+};
+
+// ---- activations ---------------------------------------------------------------
+// exp through v_exp_f32 (2^x): the rounded product p log2(e) costs |p| 2^-24
+// relative, below 2^-17 wherever the result is not already 0 or infinite, far
+// under the half unit of a 16-bit output; so does v_rcp_f32 (one ulp).
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x));
+}
+// normal distribution function; erfc keeps the digits of a far negative tail
+__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -0.70710678f); }
+// (1 + tanh a) / 2 = sigmoid(2 a), a = sqrt(2/pi) (x + 0.044715 x^3)
+__device__ __forceinline__ float gelu_tanh_gate(float x) {
+  return sigmoid(1.59576912f * fmaf(0.044715f * x * x, x, x));
+}
+
+__device__ __forceinline__ float act_of(float p, int act) {
+  switch (act) {
+    case ECHO_ACT_RELU: return p <= 0.f ? 0.f : p;
+    case ECHO_ACT_GELU: return p * normal_cdf(p);
+    case ECHO_ACT_GELU_TANH: return p * gelu_tanh_gate(p);
+    case ECHO_ACT_SILU: return p * sigmoid(p);
+    default: return p;
+  }
+}
+// value and slope
+__device__ __forceinline__ void act_slope(float p, int act, float& v, float& d) {
+  switch (act) {
+    case ECHO_ACT_RELU:
+      v = p <= 0.f ? 0.f : p;
+      d = p > 0.f ? 1.f : 0.f;
+      return;
+    case ECHO_ACT_GELU: {
+      const float c = normal_cdf(p);
+      v = p * c;
+      d = fmaf(p * 0.39894228f, exp_fast(-0.5f * p * p), c);
+      return;
+    }
+    case ECHO_ACT_GELU_TANH: {
+      const float s = gelu_tanh_gate(p);
+      v = p * s;
+      d = fmaf(v * (1.f - s), 1.59576912f * fmaf(0.134145f, p * p, 1.f), s);
+      return;
+    }
+    case ECHO_ACT_SILU: {
+      const float s = sigmoid(p);
+      v = p * s;
+      d = fmaf(v, 1.f - s, s);
+      return;
+    }
+    default:
+      v = p;
+      d = 1.f;
+  }
+}
+
+// ---- epilogue --------------------------------------------------------------------
+// g: W neighbouring sums of row i from column j (gated: the gate's, and u the
+// up rows'), of which the first n exist.
+template <typename T, int W, bool GATED>
+__device__ __forceinline__ void finish(const TileArgs& a, int64_t i, int64_t j, int n, float (&g)[W],
+                                       float (&u)[W]) {
+  const int64_t cols = GATED ? 2 * a.J : a.J;
+  float f[W];
+  if (a.bias) {
+    load_w<T, W>((const T*)a.bias + j, n, f);
+#pragma unroll
+    for (int e = 0; e < W; ++e) g[e] += f[e];
+    if constexpr (GATED) {
+      load_w<T, W>((const T*)a.bias + a.J + j, n, f);
+#pragma unroll
+      for (int e = 0; e < W; ++e) u[e] += f[e];
+    }
+  }
+  if (a.p) {
+    T* p = (T*)a.p + i * cols + j;
+    store_w<T, W>(p, n, g);
+    if constexpr (GATED) store_w<T, W>(p + a.J, n, u);
+  }
+  if (GATED || a.act != ECHO_ACT_NONE) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) g[e] = act_of(g[e], a.act);
+  }
+  if constexpr (GATED) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) g[e] *= u[e];
+  }
+  if (a.residual) {
+    load_w<T, W>((const T*)a.residual + i * a.ldr + j, n, f);
+#pragma unroll
+    for (int e = 0; e < W; ++e) g[e] += f[e];
+  }
+  store_w<T, W>((T*)a.out + i * a.ldo + j, n, g);
+}
+
+// ---- operand tiles ---------------------------------------------------------------
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c, bf16_t) {
+  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b),
+                                                 c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c, f16_t) {
+  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b),
+                                                c, 0, 0, 0);
+}
+
+// Row of an operand's tile that position rho (0..15) of its 16-row fragment t
+// stands for.  Paired fragments share 32 rows so that a lane's sums of both are
+// eight neighbours; else a fragment is 16 neighbouring rows.
+template <bool PAIRED>
+__device__ __forceinline__ int fragment_row(int t, int rho) {
+  if (PAIRED) return (t >> 1) * 32 + (rho >> 2) * 8 + (t & 1) * 4 + (rho & 3);
+  return t * 16 + rho;
+}
+
+// R rows of an operand by kC of the contraction, NT threads staging it.
+template <bool ACROSS, bool PAIRED, int R, int NT>
+struct OperandTile {
+  static constexpr int kChunks = R * kC / 8;  // 16-byte chunks
+  static constexpr int kPer = kChunks / NT;   // of a thread
+  static constexpr int kRow = ACROSS ? R / 8 : kC / 8;  // chunks of a stored row
+  static_assert(kChunks % NT == 0, "chunks per thread");
+
+  static __device__ __forceinline__ int spread(int row) {
+    if (ACROSS) return ((row & 3) | (row >> 1 & 4)) & (R / 16 - 1);
+    return PAIRED ? (row & 3) | (row >> 1 & 4) : row & 7;
+  }
+  // chunk of its row that is stored at place pc of row `row`, and back
+  static __device__ __forceinline__ int place(int row, int pc) {
+    return ACROSS ? pc ^ (spread(row) << 1) : pc ^ spread(row);
+  }
+  // eight elements c = kk*32 + 8 g .. of the rows of fragment t (lane = 16 g + rho)
+  static __device__ __forceinline__ s16x8 fragment(const short* lds, int t, int kk, int lane, int base) {
+    const int g = lane >> 4, rho = lane & 15;
+    if constexpr (!ACROSS) {
+      const int row = base + fragment_row<PAIRED>(t, rho);
+      return *reinterpret_cast<const s16x8*>(lds + row * kC + place(row, kk * 4 + g) * 8);
+    } else {
+      static_assert(!PAIRED || !ACROSS, "transposed fragments are 16 neighbouring rows");
+      typedef __attribute__((address_space(3))) s16x4 lds4;
+      s16x4 h[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c = kk * 32 + g * 8 + q * 4 + (rho >> 2);
+        const int chunk = (base + t * 16) / 8 + (rho >> 1 & 1);
+        const short* p = lds + c * R + place(c, chunk) * 8 + (rho & 1) * 4;
+        h[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
+      }
+      return __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// B's row for row r of its tile: gated, runs of 32 gate rows and the 32 up rows
+// of the same outputs alternate, so one lane holds both sums of an output.
+template <bool GATED>
+__device__ __forceinline__ void b_row(int r, int64_t j0, int64_t J, int64_t& row, bool& there) {
+  if (!GATED) {
+    row = j0 + r;
+    there = row < J;
+  } else {
+    const int64_t j = j0 + (r >> 6) * 32 + (r & 31);
+    there = j < J;
+    row = (r >> 5 & 1) ? J + j : j;
+  }
+}
+
+// Workgroups are dealt to the 8 XCDs in turn; renumbered, an XCD takes one run
+// of tiles, and runs go over kBand tile rows before the next tile column, so
+// that the tiles in flight on an XCD share operands in its L2.
+constexpr uint32_t kBand = 8;
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t nb, uint32_t tiles_i, uint32_t tiles_j,
+                                        uint32_t& ti, uint32_t& tj) {
+  const uint32_t xcd = b % 8, k = b / 8, per = nb / 8, extra = nb % 8;
+  const uint32_t t = xcd * per + (xcd < extra ? xcd : extra) + k;
+  const uint32_t band = t / (kBand * tiles_j), first = band * kBand;
+  const uint32_t rows = min(kBand, tiles_i - first), r = t - first * tiles_j;
+  ti = first + r % rows;
+  tj = r / rows;
+}
+
+}  // namespace echo

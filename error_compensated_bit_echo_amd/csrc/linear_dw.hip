@@ -1,0 +1,16 @@
+// linear_dw.hip -- dw = dp^T x: the tile kernel's instances.
+#include "linear_tile.h"
+
+namespace echo {
+
+template <typename T>
+static int product(const TileArgs& a, int edge, hipStream_t s) {
+  if (edge == 128) return launch_tile<T, true, true, 128, 128, 2, 2, false>(a, s);
+  return launch_tile<T, true, true, 64, 64, 2, 2, false>(a, s);
+}
+
+int tile_dw(const TileArgs& a, int32_t dtype, int edge, hipStream_t s) {
+  return dtype == ECHO_BF16 ? product<bf16_t>(a, edge, s) : product<f16_t>(a, edge, s);
+}
+
+}  // namespace echo

@@ -1,0 +1,164 @@
+// linear_tile.h -- the tile kernel of the matrix products (linear_device.h has
+// its parts and the layout).  Each product's source file instantiates it.
+#pragma once
+
+#include "host_checks.h"
+#include "linear_device.h"
+
+namespace echo {
+namespace {
+
+// eight elements of which the first n exist, the others 0
+template <typename T>
+__device__ __forceinline__ u32x4 raw8(const T* p, int64_t n) {
+  if (n >= 8) return *reinterpret_cast<const u32x4_a2*>(p);
+  u32x4 w = {0, 0, 0, 0};
+  if (n > 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (i % 2 * 16);
+  }
+  return w;
+}
+
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED>
+__global__ __launch_bounds__(64 * WI * WJ) void k_tile(TileArgs a) {
+  constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
+  constexpr bool PAIRED = !TB;
+  constexpr int OUT = GATED ? BJ / 2 : BJ;  // outputs of a tile row
+  static_assert(!PAIRED || TJ % (GATED ? 4 : 2) == 0, "fragments of a wavefront");
+  typedef OperandTile<TA, false, BI, NT> A;
+  typedef OperandTile<TB, PAIRED, BJ, NT> B;
+  __shared__ short lds[2][(BI + BJ) * kC];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+  const uint32_t tiles = a.tiles_i * a.tiles_j;
+  uint32_t ti, tj, split = 0;
+  if (a.splits > 1) split = blockIdx.x / tiles;
+  tile_of(blockIdx.x - split * tiles, tiles, a.tiles_i, a.tiles_j, ti, tj);
+  const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * OUT;
+  const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
+  const int steps = (int)((c1 - c0 + kC - 1) / kC);
+
+  u32x4 ra[A::kPer], rb[B::kPer];
+  auto load = [&](int64_t c) {
+#pragma unroll
+    for (int i = 0; i < A::kPer; ++i) {
+      const int q = i * NT + tid, r = q / A::kRow, col = A::place(r, q % A::kRow) * 8;
+      if constexpr (TA) {
+        const int64_t n = c + r < c1 ? a.I - (i0 + col) : 0;
+        ra[i] = raw8((const T*)a.a + (c + r) * a.lda + i0 + col, n);
+      } else {
+        const int64_t n = i0 + r < a.I ? c1 - (c + col) : 0;
+        ra[i] = raw8((const T*)a.a + (i0 + r) * a.lda + c + col, n);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < B::kPer; ++i) {
+      const int q = i * NT + tid, r = q / B::kRow, col = B::place(r, q % B::kRow) * 8;
+      if constexpr (TB) {
+        const int64_t n = c + r < c1 ? a.J - (j0 + col) : 0;
+        rb[i] = raw8((const T*)a.b + (c + r) * a.ldb + j0 + col, n);
+      } else {
+        int64_t row;
+        bool there;
+        b_row<GATED>(r, j0, a.J, row, there);
+        rb[i] = raw8((const T*)a.b + row * a.ldb + c + col, there ? c1 - (c + col) : 0);
+      }
+    }
+  };
+  auto stage = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < A::kPer; ++i) *(u32x4*)(lds[s] + (i * NT + tid) * 8) = ra[i];
+#pragma unroll
+    for (int i = 0; i < B::kPer; ++i) *(u32x4*)(lds[s] + BI * kC + (i * NT + tid) * 8) = rb[i];
+  };
+
+  f32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (steps > 0) {
+    load(c0);
+    stage(0);
+  }
+  __syncthreads();
+  for (int s = 0; s < steps; ++s) {
+    if (s + 1 < steps) load(c0 + (int64_t)(s + 1) * kC);
+    const short *la = lds[s & 1], *lb = lds[s & 1] + BI * kC;
+#pragma unroll
+    for (int kk = 0; kk < kC / 32; ++kk) {
+      s16x8 fa[TI], fb[TJ];
+#pragma unroll
+      for (int i = 0; i < TI; ++i) fa[i] = A::fragment(la, i, kk, lane, wi);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) fb[j] = B::fragment(lb, j, kk, lane, wj);
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[j], fa[i], acc[i][j], T{});
+    }
+    if (s + 1 < steps) stage((s + 1) & 1);
+    __syncthreads();
+  }
+
+  // Lane 16 g + rho holds row rho of each of A's fragments.  Along j it holds
+  // four sums of one fragment of B or, paired, eight of two.
+  const int g = lane >> 4, rho = lane & 15;
+  const int64_t cols = GATED ? 2 * a.J : a.J;
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int64_t row = i0 + wi + i * 16 + rho;
+    if (row >= a.I) continue;
+    constexpr int W = PAIRED ? 8 : 4, STEP = GATED ? 4 : PAIRED ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < TJ; j += STEP) {
+      float v[W], u[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        v[e] = acc[i][j + e / 4][e % 4];
+        u[e] = GATED ? acc[i][(j + 2) % TJ + e / 4][e % 4] : 0.f;
+      }
+      const int64_t col = j0 + (GATED ? (wj + j * 16) / 2 : wj + j * 16) + g * W;
+      if (col >= a.J) continue;
+      const int n = (int)min(a.J - col, (int64_t)W);
+      if (a.splits > 1) {
+        float* p = a.part + ((int64_t)split * a.I + row) * cols + col;
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (e < n) {
+            p[e] = v[e];
+            if (GATED) p[a.J + e] = u[e];
+          }
+      } else {
+        finish<T, W, GATED>(a, row, col, n, v, u);
+      }
+    }
+  }
+}
+
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED>
+int launch_tile(TileArgs a, hipStream_t s) {
+  const int64_t out = GATED ? BJ / 2 : BJ;
+  const int64_t ti = (a.I + BI - 1) / BI, tj = (a.J + out - 1) / out;
+  constexpr int NT = 64 * WI * WJ;
+  if (ti * tj == 0) return ECHO_SUCCESS;
+  if (ti * tj > (int64_t)(0xFFFFFFFFu / NT) / a.splits) return ECHO_ERR_SHAPE;
+  a.tiles_i = (uint32_t)ti;
+  a.tiles_j = (uint32_t)tj;
+  return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED>, dim3(a.tiles_i * a.tiles_j * a.splits),
+                dim3(NT), s, a);
+}
+
+}  // namespace
+
+// The products, by the tile's edge (128 or 64), one source file each.
+int tile_forward(const TileArgs& a, int32_t dtype, bool gated, int edge, hipStream_t s);
+int tile_dx(const TileArgs& a, int32_t dtype, int edge, hipStream_t s);
+int tile_dw(const TileArgs& a, int32_t dtype, int edge, hipStream_t s);
+
+}  // namespace echo

@@ -18,8 +18,8 @@
  *     are multiples of 16 bytes are faster.
  *   - Sums, statistics and everything between reading an input and writing an
  *     output are binary32; each output is rounded once, to nearest even.
- *     Two named exceptions: the backward products read the gradient of the
- *     pre-activation rounded to `dtype` (the matrix cores' operand type).
+ *     One exception: the products of echo_linear_backward read the gradient of
+ *     the pre-activation rounded to `dtype`, the matrix cores' operand type.
  *   - No atomics: the same inputs give the same bits on every call.
  *   - inf and NaN go through as the formulas have them: a row that holds one
  *     spoils that row of the norms and nothing else, an operand of a product
@@ -105,6 +105,50 @@ int echo_norm_backward(const echo_norm_desc* d, const void* dz, const void* dh_o
                        void* dy, void* dgate, void* dw_post, void* db_post, void* dw_pre,
                        void* db_pre, void* workspace, int64_t workspace_bytes,
                        echo_stream_t stream);
+
+/* A matrix product with its epilogue: p = x w^T + bias and out = act(p) +
+ * residual, or, gated, out = act(p_gate) (.) p_up + residual.  x is m rows of
+ * k, out m rows of n, w n rows of k: row j holds the weights of output j.
+ * Gated, w has 2n rows, the gate's first and the up rows behind them; bias,
+ * p, and the gradients of w and bias have the same order. */
+typedef struct echo_linear_desc {
+  int64_t m, n, k;   /* each may be 0; m <= ECHO_MAX_ROWS, k and the rows of w <= ECHO_MAX_PITCH */
+  int64_t ld_x;      /* row pitch of x */
+  int64_t ld_w;      /* row pitch of w */
+  int64_t ld_out;    /* row pitch of out, and of its gradient */
+  int64_t ld_r;      /* row pitch of residual */
+  int32_t dtype;     /* of every tensor: ECHO_BF16 or ECHO_F16 */
+  int32_t act;       /* ECHO_ACT_* */
+  int32_t gated;     /* 0 or 1 */
+  int32_t reserved;  /* 0 */
+} echo_linear_desc;
+
+/* Bytes of workspace echo_linear needs for this shape (0 for many), or a
+ * negative ECHO_ERR_*. */
+int64_t echo_linear_workspace(const echo_linear_desc* d);
+
+/* The forward product.  bias (the rows of w), residual [m, n] and p (dense
+ * [m, rows of w]: the sums with bias before the activation, kept for the
+ * backward call) may be NULL.  out may equal residual exactly. */
+int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const void* bias,
+                const void* residual, void* out, void* p, void* workspace,
+                int64_t workspace_bytes, echo_stream_t stream);
+
+/* Bytes of workspace echo_linear_backward needs, or a negative ECHO_ERR_*. */
+int64_t echo_linear_backward_workspace(const echo_linear_desc* d);
+
+/* Gradients of echo_linear from dout (pitch ld_out) and the forward call's x,
+ * w and p:
+ *   dp = dout (.) act'(p), or, gated, (dout (.) p_up (.) act'(p_gate),
+ *        dout (.) act(p_gate));   rounded to dtype for the two products
+ *   dx = dp w (dense [m, k]);  dw = dp^T x (dense, the shape of w);
+ *   dbias = sum over the rows of dp (of its binary32 values)
+ * The residual's gradient is dout itself.  Each of dx, dw, dbias may be NULL to
+ * skip it; asked for, it is written whole, zeros where the sum is empty.  p is
+ * read unless act is NONE and gated 0 (then it may be NULL). */
+int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void* x,
+                         const void* w, const void* p, void* dx, void* dw, void* dbias,
+                         void* workspace, int64_t workspace_bytes, echo_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -89,6 +89,61 @@ def test_norm_backward_rejections():
         B.echo_norm_backward_workspace(4, 20000)
 
 
+def ldesc(m=8, n=16, k=32, ld_x=0, ld_w=0, ld_out=0, ld_r=0, dt=0, act=0, gated=0):
+    return B.EchoLinearDescC(m, n, k, ld_x, ld_w, ld_out, ld_r, dt, act, gated, 0)
+
+
+def lin(d, x=A, w=2 * A, bias=None, residual=None, out=3 * A, p=None, ws=None, n=0):
+    return B.lib.echo_linear(C.byref(d) if d else None, x, w, bias, residual, out, p, ws, n, None)
+
+
+BAD_SHAPES = (dict(m=-1), dict(n=-1), dict(k=-1), dict(m=(1 << 31) + 1), dict(k=(1 << 21) + 1), dict(n=(1 << 21) + 1),
+              dict(n=(1 << 20) + 1, gated=1), dict(ld_x=31), dict(ld_w=5), dict(ld_out=15), dict(ld_r=15),
+              dict(ld_x=(1 << 21) + 8))
+BAD_TYPES = (dict(dt=2), dict(dt=-1), dict(act=5), dict(act=-1), dict(gated=2))
+
+
+def test_linear_rejections():
+    assert lin(None) == -1
+    for bad in BAD_SHAPES:
+        assert lin(ldesc(**bad)) == -2, bad
+        assert B.lib.echo_linear_workspace(C.byref(ldesc(**bad))) == -2
+        assert B.lib.echo_linear_backward_workspace(C.byref(ldesc(**bad))) == -2
+    for bad in BAD_TYPES:
+        assert lin(ldesc(**bad)) == -8, bad
+    for name in ("x", "w", "out"):
+        assert lin(ldesc(), **{name: None}) == -1, name
+    for name in ("x", "w", "bias", "residual", "out", "p"):
+        assert lin(ldesc(), **{name: 4 * A + 1}) == -3, name
+    assert lin(ldesc(), out=A + 64) == -6 and lin(ldesc(), out=2 * A) == -6 and lin(ldesc(), p=3 * A + 16) == -6
+    assert lin(ldesc(), residual=3 * A + 2) == -6          # over out but not equal to it
+    assert lin(ldesc(ld_x=100), out=A + 1400) == -6        # within x's last rows, by its pitch
+    assert lin(ldesc(m=0), x=None, w=None, out=None) == 0
+    assert lin(ldesc(n=0), x=None, w=None, out=None) == 0
+
+
+def linb(d, dout=A, x=2 * A, w=3 * A, p=None, dx=4 * A, dw=5 * A, db=None, ws=6 * A, n=1 << 30):
+    return B.lib.echo_linear_backward(C.byref(d) if d else None, dout, x, w, p, dx, dw, db, ws, n, None)
+
+
+def test_linear_backward_rejections():
+    assert linb(None) == -1
+    for bad in BAD_SHAPES:
+        assert linb(ldesc(**bad)) == -2, bad
+    for bad in BAD_TYPES:
+        assert linb(ldesc(**bad)) == -8, bad
+    for name in ("dout", "x", "w"):
+        assert linb(ldesc(), **{name: None}) == -1, name
+    assert linb(ldesc(act=4)) == -1 and linb(ldesc(gated=1)) == -1    # p missing
+    need = B.echo_linear_backward_workspace(8, 16, 32, act="silu")
+    assert need > 0 and linb(ldesc(act=4), p=7 * A, n=need - 1) == -9 and linb(ldesc(act=4), p=7 * A, ws=None) == -1
+    for name in ("dout", "x", "w", "p", "dx", "dw", "db"):
+        assert linb(ldesc(act=4), **{"p": 7 * A, name: 8 * A + 1}) == -3, name
+    assert linb(ldesc(), ws=6 * A + 8) == -3
+    assert linb(ldesc(), dx=A) == -6 and linb(ldesc(), dw=4 * A + 2) == -6 and linb(ldesc(), db=3 * A) == -6
+    assert linb(ldesc(act=4), p=7 * A, dx=6 * A) == -6                 # over the workspace
+
+
 def test_binding_refuses_before_the_library():
     t = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU tensor"):
@@ -97,3 +152,11 @@ def test_binding_refuses_before_the_library():
         B.echo_norm(t.to(torch.int16), t, t, t, stream=0)
     with pytest.raises(ValueError, match="is not one of"):
         B._code(B.NORMS, "batch", "pre")
+    with pytest.raises(ValueError, match="GPU tensor"):
+        B.echo_linear(t, t, torch.zeros(4, 4, dtype=torch.bfloat16), stream=0)
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
+        B.echo_linear(t.float(), t.float(), t, stream=0)
+    with pytest.raises(ValueError, match="even number of rows"):
+        B.echo_linear(t, torch.zeros(5, 64, dtype=torch.bfloat16), t, gated=True, stream=0)
+    with pytest.raises(ValueError, match="is not one of"):
+        B.echo_linear_workspace(4, 4, 4, act="swish")

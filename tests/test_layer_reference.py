@@ -67,3 +67,38 @@ def test_the_bound_is_tight_enough_to_see_a_wrong_value():
     R.close(got, [1.0, 2.0, 3.0], [1.0, 2.0, 3.0], 4, "same")
     with pytest.raises(AssertionError):
         R.close(got, [1.0, 2.0, 3.0 + 3e-6], [1.0, 2.0, 3.0], 4, "off by 1e-6")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kind", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_linear_gradients_follow_the_forward_formula(kind, gated):
+    gen = torch.Generator().manual_seed(21)
+    m, n, k = 5, 4, 7
+    rows = 2 * n if gated else n
+    x, w, bias = _leaf(gen, m, k), _leaf(gen, rows, k), _leaf(gen, rows)
+    residual = torch.randn(m, n, generator=gen, dtype=torch.float64)
+    dout = torch.randn(m, n, generator=gen, dtype=torch.float64)
+    f = {"none": lambda v: v, "relu": torch.relu, "gelu": torch.nn.functional.gelu,
+         "gelu_tanh": lambda v: torch.nn.functional.gelu(v, approximate="tanh"),
+         "silu": torch.nn.functional.silu}[kind]
+    p = x @ w.T + bias
+    out = (f(p[:, :n]) * p[:, n:] if gated else f(p)) + residual
+    got = R.linear_forward(x, w, bias, residual, kind, gated)
+    assert np.allclose(got["out"][0], out.detach().numpy(), rtol=1e-12, atol=1e-13)
+    (out * dout).sum().backward()
+    back = R.linear_backward(dout, x, w, p, kind, gated)
+    for name, leaf in (("dx", x), ("dw", w), ("dbias", bias)):
+        assert np.allclose(back[name][0], leaf.grad.numpy(), rtol=1e-10, atol=1e-12), name
+    # a central difference along one direction of x, of w and of bias
+    rng = np.random.default_rng(8)
+    for name in ("dx", "dw", "dbias"):
+        at = {"dx": x.detach().numpy(), "dw": w.detach().numpy(), "dbias": bias.detach().numpy()}
+        way, step = rng.standard_normal(at[name].shape), 1e-6
+
+        def objective(s):
+            v = {q: torch.from_numpy(a + s * way if q == name else a) for q, a in at.items()}
+            o = R.linear_forward(v["dx"], v["dw"], v["dbias"], residual, kind, gated)["out"][0]
+            return float((o * dout.numpy()).sum())
+
+        diff, along = (objective(step) - objective(-step)) / (2 * step), float((back[name][0] * way).sum())
+        assert abs(diff - along) <= 1e-6 * max(1.0, abs(along)), (name, diff, along)
