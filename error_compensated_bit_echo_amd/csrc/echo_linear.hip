@@ -163,9 +163,11 @@ BackPlan plan_back(const echo_linear_desc* d, const Geometry& g) {
 }
 
 int edge_of(int64_t I, int64_t cols) {
-  // a tile of 128 reads half as much per output; 64 fills the 256 compute
+  // a larger tile reads less per output; a smaller one fills the 256 compute
   // units where there are few tiles
-  return ((I + 127) / 128) * ((cols + 127) / 128) >= 256 ? 128 : 64;
+  for (int edge = 256; edge > 64; edge /= 2)
+    if (((I + edge - 1) / edge) * ((cols + edge - 1) / edge) >= 192) return edge;
+  return 64;
 }
 
 }  // namespace

@@ -5,8 +5,13 @@ namespace echo {
 
 template <typename T>
 static int product(const TileArgs& a, int edge, hipStream_t s) {
-  if (edge == 128) return launch_tile<T, true, true, 128, 128, 2, 2, false>(a, s);
-  return launch_tile<T, true, true, 64, 64, 2, 2, false>(a, s);
+  if (chunked<true, true>(a)) {
+    if (edge == 256) return launch_tile<T, true, true, 256, 256, 2, 4, false, true>(a, s);
+    if (edge == 128) return launch_tile<T, true, true, 128, 128, 2, 2, false, true>(a, s);
+    return launch_tile<T, true, true, 64, 64, 2, 2, false, true>(a, s);
+  }
+  if (edge >= 128) return launch_tile<T, true, true, 128, 128, 2, 2, false, false>(a, s);
+  return launch_tile<T, true, true, 64, 64, 2, 2, false, false>(a, s);
 }
 
 int tile_dw(const TileArgs& a, int32_t dtype, int edge, hipStream_t s) {

@@ -3,13 +3,21 @@
 
 namespace echo {
 
+template <typename T, bool GATED>
+static int forward(const TileArgs& a, int edge, hipStream_t s) {
+  constexpr int SI = GATED ? 4 : 2, SJ = GATED ? 1 : 2;  // a gated run is 64 rows of w, in one wavefront
+  if (chunked<false, false>(a)) {
+    if (edge == 256) return launch_tile<T, false, false, 256, 256, 2, 4, GATED, true>(a, s);
+    if (edge == 128) return launch_tile<T, false, false, 128, 128, 2, 2, GATED, true>(a, s);
+    return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, true>(a, s);
+  }
+  if (edge >= 128) return launch_tile<T, false, false, 128, 128, 2, 2, GATED, false>(a, s);
+  return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, false>(a, s);
+}
+
 template <typename T>
 static int forward(const TileArgs& a, bool gated, int edge, hipStream_t s) {
-  if (edge == 128)
-    return gated ? launch_tile<T, false, false, 128, 128, 2, 2, true>(a, s)
-                 : launch_tile<T, false, false, 128, 128, 2, 2, false>(a, s);
-  return gated ? launch_tile<T, false, false, 64, 64, 4, 1, true>(a, s)
-               : launch_tile<T, false, false, 64, 64, 2, 2, false>(a, s);
+  return gated ? forward<T, true>(a, edge, s) : forward<T, false>(a, edge, s);
 }
 
 int tile_forward(const TileArgs& a, int32_t dtype, bool gated, int edge, hipStream_t s) {

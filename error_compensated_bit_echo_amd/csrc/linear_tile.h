@@ -21,6 +21,45 @@ __device__ __forceinline__ u32x4 raw8(const T* p, int64_t n) {
   return w;
 }
 
+// A wavefront's sums to the epilogue, or to a split's partial sums.  Lane
+// 16 g + rho holds row rho of each of A's fragments; along j it holds four sums
+// of one fragment of B or, paired, eight of two.
+template <typename T, bool PAIRED, bool GATED, int TI, int TJ>
+__device__ __forceinline__ void write_tile(const TileArgs& a, const f32x4 (&acc)[TI][TJ], int64_t i0,
+                                           int64_t j0, uint32_t split, int lane) {
+  const int g = lane >> 4, rho = lane & 15;
+  const int64_t cols = GATED ? 2 * a.J : a.J;
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int64_t row = i0 + i * 16 + rho;
+    if (row >= a.I) continue;
+    constexpr int W = PAIRED ? 8 : 4, STEP = GATED ? 4 : PAIRED ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < TJ; j += STEP) {
+      float v[W], u[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        v[e] = acc[i][j + e / 4][e % 4];
+        u[e] = GATED ? acc[i][(j + 2) % TJ + e / 4][e % 4] : 0.f;
+      }
+      const int64_t col = j0 + (GATED ? j * 8 : j * 16) + g * W;
+      if (col >= a.J) continue;
+      const int n = (int)min(a.J - col, (int64_t)W);
+      if (a.splits > 1) {
+        float* p = a.part + ((int64_t)split * a.I + row) * cols + col;
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (e < n) {
+            p[e] = v[e];
+            if (GATED) p[a.J + e] = u[e];
+          }
+      } else {
+        finish<T, W, GATED>(a, row, col, n, v, u);
+      }
+    }
+  }
+}
+
 template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED>
 __global__ __launch_bounds__(64 * WI * WJ) void k_tile(TileArgs a) {
   constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
@@ -106,42 +145,153 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_tile(TileArgs a) {
     __syncthreads();
   }
 
-  // Lane 16 g + rho holds row rho of each of A's fragments.  Along j it holds
-  // four sums of one fragment of B or, paired, eight of two.
-  const int g = lane >> 4, rho = lane & 15;
-  const int64_t cols = GATED ? 2 * a.J : a.J;
-#pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const int64_t row = i0 + wi + i * 16 + rho;
-    if (row >= a.I) continue;
-    constexpr int W = PAIRED ? 8 : 4, STEP = GATED ? 4 : PAIRED ? 2 : 1;
-#pragma unroll
-    for (int j = 0; j < TJ; j += STEP) {
-      float v[W], u[W];
-#pragma unroll
-      for (int e = 0; e < W; ++e) {
-        v[e] = acc[i][j + e / 4][e % 4];
-        u[e] = GATED ? acc[i][(j + 2) % TJ + e / 4][e % 4] : 0.f;
-      }
-      const int64_t col = j0 + (GATED ? (wj + j * 16) / 2 : wj + j * 16) + g * W;
-      if (col >= a.J) continue;
-      const int n = (int)min(a.J - col, (int64_t)W);
-      if (a.splits > 1) {
-        float* p = a.part + ((int64_t)split * a.I + row) * cols + col;
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (e < n) {
-            p[e] = v[e];
-            if (GATED) p[a.J + e] = u[e];
-          }
-      } else {
-        finish<T, W, GATED>(a, row, col, n, v, u);
-      }
-    }
-  }
+  write_tile<T, PAIRED, GATED, TI, TJ>(a, acc, i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
+// One 16-byte chunk per lane from memory straight into LDS, the wavefront's 64
+// chunks in lane order from `lds` on; chunks past the descriptor's range
+// arrive as zeros.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, short* lds, int offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, offset, 0,
+                                           0, 0);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t range_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes < 0 ? 0 : (int)bytes, 0x00020000);
+}
+
+// wait until this wavefront's chunks have arrived in LDS
+__device__ __forceinline__ void dma_wait() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+
+// The same tile fed by direct loads into LDS, for operands whose 16-byte chunks
+// are aligned and, along c, whole.  While one stage is multiplied the next one
+// arrives; no register holds a chunk on its way.
 template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED>
+__global__ __launch_bounds__(64 * WI * WJ) void k_tile_dma(TileArgs a) {
+  constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
+  constexpr bool PAIRED = !TB;
+  constexpr int OUT = GATED ? BJ / 2 : BJ;
+  static_assert(!PAIRED || TJ % (GATED ? 4 : 2) == 0, "fragments of a wavefront");
+  typedef OperandTile<TA, false, BI, NT> A;
+  typedef OperandTile<TB, PAIRED, BJ, NT> B;
+  __shared__ short lds0[(BI + BJ) * kC], lds1[(BI + BJ) * kC];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+  const uint32_t tiles = a.tiles_i * a.tiles_j;
+  uint32_t ti, tj, split = 0;
+  if (a.splits > 1) split = blockIdx.x / tiles;
+  tile_of(blockIdx.x - split * tiles, tiles, a.tiles_i, a.tiles_j, ti, tj);
+  const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * OUT;
+  const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
+  const int steps = (int)((c1 - c0 + kC - 1) / kC);
+  const int64_t rows_a = min(a.I - i0, (int64_t)BI), rows_b = min(a.J - j0, (int64_t)OUT);
+
+  // Byte offsets of the thread's chunks.  Along c they move by a step's bytes
+  // and the ranges stay (a tile's rows span less than 2^31 bytes); across c the
+  // ranges move and the offsets stay.
+  int oa[A::kPer], ob[B::kPer];
+  int ca[A::kPer], cb[B::kPer];  // along c: the chunk's first element in the step
+#pragma unroll
+  for (int i = 0; i < A::kPer; ++i) {
+    const int q = i * NT + tid, r = q / A::kRow;
+    ca[i] = A::place(r, q % A::kRow) * 8;
+    oa[i] = (int)(r * a.lda + ca[i]) * 2;
+  }
+#pragma unroll
+  for (int i = 0; i < B::kPer; ++i) {
+    const int q = i * NT + tid, r = q / B::kRow;
+    cb[i] = B::place(r, q % B::kRow) * 8;
+    ob[i] = (int)((GATED ? (r >> 6) * 32 + (r & 31) : r) * a.ldb + cb[i]) * 2;
+  }
+  const T* pa = (const T*)a.a + (TA ? c0 * a.lda + i0 : i0 * a.lda + c0);
+  const T* pb = (const T*)a.b + (TB ? c0 * a.ldb + j0 : j0 * a.ldb + c0);
+  constexpr int kPast = 0x7FFFFFF0;  // an offset past every range
+  auto stage = [&](short* lds, int s) {
+    const int64_t left = c1 - c0 - (int64_t)s * kC;  // of the contraction, from this step on
+    const bool tail = left < kC;
+    if constexpr (TA) {
+      // a range ends with whole words: an odd last column's word is its own row's
+      const auto r = range_of(pa + (int64_t)s * kC * a.lda,
+                              (((min(left, (int64_t)kC) - 1) * a.lda + (a.I - i0)) * 2 + 2) & ~(int64_t)3);
+#pragma unroll
+      for (int i = 0; i < A::kPer; ++i) dma16(r, lds + (i * NT + wave * 64) * 8, oa[i]);
+    } else {
+      const auto r = range_of(pa, ((rows_a - 1) * a.lda + (c1 - c0)) * 2);
+#pragma unroll
+      for (int i = 0; i < A::kPer; ++i) {
+        const int o = oa[i] + s * kC * 2;
+        dma16(r, lds + (i * NT + wave * 64) * 8, tail && ca[i] >= left ? kPast : o);
+      }
+    }
+    short* lb = lds + BI * kC;
+    if constexpr (TB) {
+      const auto r = range_of(pb + (int64_t)s * kC * a.ldb,
+                              (((min(left, (int64_t)kC) - 1) * a.ldb + (a.J - j0)) * 2 + 2) & ~(int64_t)3);
+#pragma unroll
+      for (int i = 0; i < B::kPer; ++i) dma16(r, lb + (i * NT + wave * 64) * 8, ob[i]);
+    } else {
+      const int64_t bytes = ((rows_b - 1) * a.ldb + (c1 - c0)) * 2;
+      const auto r = range_of(pb, bytes);
+      const auto up = range_of(GATED ? pb + a.J * a.ldb : pb, bytes);
+#pragma unroll
+      for (int i = 0; i < B::kPer; ++i) {
+        const int o = ob[i] + s * kC * 2;
+        // a wavefront's 64 chunks are eight rows, all of one half of a gated run
+        const bool is_up = GATED && ((i * NT + wave * 64) / B::kRow >> 5 & 1);
+        dma16(is_up ? up : r, lb + (i * NT + wave * 64) * 8, tail && cb[i] >= left ? kPast : o);
+      }
+    }
+  };
+
+  f32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const short* la) {
+    const short* lb = la + BI * kC;
+#pragma unroll
+    for (int kk = 0; kk < kC / 32; ++kk) {
+      s16x8 fa[TI], fb[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) fb[j] = B::fragment(lb, j, kk, lane, wj);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) fa[i] = A::fragment(la, i, kk, lane, wi);
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[j], fa[i], acc[i][j], T{});
+    }
+  };
+
+  if (steps > 0) stage(lds0, 0);
+  dma_wait();
+  __syncthreads();
+  for (int s = 0; s < steps; s += 2) {
+    if (s + 1 < steps) stage(lds1, s + 1);
+    multiply(lds0);
+    dma_wait();
+    __syncthreads();
+    if (s + 1 < steps) {
+      if (s + 2 < steps) stage(lds0, s + 2);
+      multiply(lds1);
+      dma_wait();
+      __syncthreads();
+    }
+  }
+  write_tile<T, PAIRED, GATED, TI, TJ>(a, acc, i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
+}
+
+// whether every 16-byte chunk of both operands is aligned and, along c, whole
+template <bool TA, bool TB>
+bool chunked(const TileArgs& a) {
+  return aligned(a.a, 16) && aligned(a.b, 16) && a.lda % 8 == 0 && a.ldb % 8 == 0 &&
+         ((TA && TB) || a.C % 8 == 0);
+}
+
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, bool DMA>
 int launch_tile(TileArgs a, hipStream_t s) {
   const int64_t out = GATED ? BJ / 2 : BJ;
   const int64_t ti = (a.I + BI - 1) / BI, tj = (a.J + out - 1) / out;
@@ -150,8 +300,9 @@ int launch_tile(TileArgs a, hipStream_t s) {
   if (ti * tj > (int64_t)(0xFFFFFFFFu / NT) / a.splits) return ECHO_ERR_SHAPE;
   a.tiles_i = (uint32_t)ti;
   a.tiles_j = (uint32_t)tj;
-  return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED>, dim3(a.tiles_i * a.tiles_j * a.splits),
-                dim3(NT), s, a);
+  const dim3 grid(a.tiles_i * a.tiles_j * a.splits);
+  if constexpr (DMA) return launch(k_tile_dma<T, TA, TB, BI, BJ, WI, WJ, GATED>, grid, dim3(NT), s, a);
+  else return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED>, grid, dim3(NT), s, a);
 }
 
 }  // namespace
