@@ -29,6 +29,9 @@
 
 namespace echo {
 
+// addresses in LDS, as such: through a generic pointer the compiler loses track
+// of which buffer a transposed read is from and waits for every load in flight
+typedef __attribute__((address_space(3))) short lds_short;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -179,11 +182,12 @@ struct OperandTile {
     return ACROSS ? pc ^ (spread(row) << 1) : pc ^ spread(row);
   }
   // eight elements c = kk*32 + 8 g .. of the rows of fragment t (lane = 16 g + rho)
-  static __device__ __forceinline__ s16x8 fragment(const short* lds, int t, int kk, int lane, int base) {
+  static __device__ __forceinline__ s16x8 fragment(const lds_short* lds, int t, int kk, int lane, int base) {
     const int g = lane >> 4, rho = lane & 15;
     if constexpr (!ACROSS) {
       const int row = base + fragment_row<PAIRED>(t, rho);
-      return *reinterpret_cast<const s16x8*>(lds + row * kC + place(row, kk * 4 + g) * 8);
+      typedef __attribute__((address_space(3))) const s16x8 lds8;
+      return *(lds8*)(lds + row * kC + place(row, kk * 4 + g) * 8);
     } else {
       static_assert(!PAIRED || !ACROSS, "transposed fragments are 16 neighbouring rows");
       typedef __attribute__((address_space(3))) s16x4 lds4;
@@ -192,7 +196,7 @@ struct OperandTile {
       for (int q = 0; q < 2; ++q) {
         const int c = kk * 32 + g * 8 + q * 4 + (rho >> 2);
         const int chunk = (base + t * 16) / 8 + (rho >> 1 & 1);
-        const short* p = lds + c * R + place(c, chunk) * 8 + (rho & 1) * 4;
+        const lds_short* p = lds + c * R + place(c, chunk) * 8 + (rho & 1) * 4;
         h[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
       }
       return __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);

@@ -6,7 +6,7 @@ namespace echo {
 template <typename T>
 static int product(const TileArgs& a, int edge, hipStream_t s) {
   if (chunked<false, true>(a)) {
-    if (edge == 256) return launch_tile<T, false, true, 256, 256, 2, 4, false, true>(a, s);
+    if (edge == 256) return launch_tile<T, false, true, 256, 256, 4, 2, false, true>(a, s);
     if (edge == 128) return launch_tile<T, false, true, 128, 128, 2, 2, false, true>(a, s);
     return launch_tile<T, false, true, 64, 64, 2, 2, false, true>(a, s);
   }

@@ -7,7 +7,7 @@ template <typename T, bool GATED>
 static int forward(const TileArgs& a, int edge, hipStream_t s) {
   constexpr int SI = GATED ? 4 : 2, SJ = GATED ? 1 : 2;  // a gated run is 64 rows of w, in one wavefront
   if (chunked<false, false>(a)) {
-    if (edge == 256) return launch_tile<T, false, false, 256, 256, 2, 4, GATED, true>(a, s);
+    if (edge == 256) return launch_tile<T, false, false, 256, 256, 4, 2, GATED, true>(a, s);
     if (edge == 128) return launch_tile<T, false, false, 128, 128, 2, 2, GATED, true>(a, s);
     return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, true>(a, s);
   }
