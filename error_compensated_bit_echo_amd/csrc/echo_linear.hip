@@ -3,6 +3,7 @@
 // echo_linear_backward (include/echo_layer.h) and the kernels beside the tile
 // kernel of linear_tile.h.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "echo_layer.h"
@@ -106,6 +107,34 @@ __global__ __launch_bounds__(1024) void k_run_sum(RunSumArgs a) {
   }
 }
 
+// ---- joining splits ---------------------------------------------------------------
+// The splits' sums added in order, then the epilogue; 8 outputs to a thread.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(kBlock) void k_join(TileArgs a) {
+  const int64_t cols = GATED ? 2 * a.J : a.J, vectors = (a.J + 7) / 8;
+  const int64_t plane = a.I * cols, items = a.I * vectors;
+  for (int64_t t = (int64_t)blockIdx.x * kBlock + threadIdx.x; t < items; t += (int64_t)gridDim.x * kBlock) {
+    const int64_t i = t / vectors, j = (t - i * vectors) * 8;
+    const int n = (int)min(a.J - j, (int64_t)8);
+    const float* p = a.part + i * cols + j;
+    float g[8], u[8], f[8];
+    load_n<true>(p, n, g);
+    if (GATED) load_n<true>(p + a.J, n, u);
+    for (uint32_t s = 1; s < a.splits; ++s) {
+      p += plane;
+      load_n<true>(p, n, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] += f[e];
+      if (GATED) {
+        load_n<true>(p + a.J, n, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] += f[e];
+      }
+    }
+    finish<T, 8, GATED>(a, i, j, n, g, u);
+  }
+}
+
 // ---- host side ---------------------------------------------------------------------
 
 struct Geometry {
@@ -141,10 +170,70 @@ int check_desc(const echo_linear_desc* d, Geometry& g) {
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// The backward pass's workspace: dp where it differs from dout, and the bias's
-// partial sums, one row for each run of rows.
+// Which tile, and into how many splits of the contraction.  The estimate of a
+// choice: a compute unit works through n workgroups of `steps` steps, at
+// `step` us a step once it has several to overlap and `alone` us with one (as
+// measured, bf16); splits cost writing and reading their binary32 sums and one
+// more launch.  It is the rule; nothing is tuned to a shape.
+struct TileCost { int bi, bj; float step, alone; };
+constexpr TileCost kChunkedCost[kTileKinds] = {
+    {256, 256, 1.65f, 1.65f}, {256, 128, 1.00f, 1.00f}, {128, 128, 0.50f, 0.62f}, {64, 64, 0.18f, 0.22f}};
+constexpr TileCost kStagedCost[kTileKinds] = {
+    {0, 0, 0, 0}, {0, 0, 0, 0}, {128, 128, 0.67f, 0.85f}, {64, 64, 0.23f, 0.50f}};
+constexpr int64_t kMostPart = INT64_C(256) << 20;  // bytes of partial sums
+
+struct Plan { int tile; int64_t splits, chunk, part_bytes; };
+
+Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
+  const int64_t steps = (C + kC - 1) / kC;
+  Plan best = {kTile64, 1, steps * kC, 0};
+  double least = 1e30;
+  for (int t = 0; t < kTileKinds; ++t) {
+    const TileCost& k = is_chunked ? kChunkedCost[t] : kStagedCost[t];
+    if (k.bi == 0) continue;
+    const double tiles = (double)((I + k.bi - 1) / k.bi) * (double)((cols + k.bj - 1) / k.bj);
+    for (int64_t splits = 1; splits <= 32; ++splits) {
+      const int64_t each = (steps + splits - 1) / splits;
+      if (splits > 1 && (each < 4 || (steps + each - 1) / each != splits)) continue;
+      const double bytes = splits > 1 ? 4.0 * (double)I * (double)cols * (double)splits : 0.0;
+      if (bytes > (double)kMostPart) break;
+      const double per_cu = ceil(tiles * (double)splits / 256.0);
+      const double busy = per_cu * k.step > k.alone ? per_cu * k.step : k.alone;
+      const double us = (double)each * busy + (splits > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
+      if (us < least) {
+        least = us;
+        best = {t, splits, each * kC, splits > 1 ? (int64_t)bytes : 0};
+      }
+    }
+  }
+  return best;
+}
+
+// partial sums of either kind of operands fit
+int64_t part_bytes(int64_t I, int64_t cols, int64_t C) {
+  const int64_t a = plan_tiles(I, cols, C, true).part_bytes, b = plan_tiles(I, cols, C, false).part_bytes;
+  return round_up(a > b ? a : b, 16);
+}
+
+template <bool GATED>
+int run_join(const TileArgs& a, int32_t dtype, hipStream_t s) {
+  const uint64_t items = (uint64_t)a.I * (uint64_t)((a.J + 7) / 8);
+  const dim3 grid(blocks_for_items(items)), block(kBlock);
+  return dtype == ECHO_BF16 ? launch(k_join<bf16_t, GATED>, grid, block, s, a)
+                            : launch(k_join<f16_t, GATED>, grid, block, s, a);
+}
+
+void apply(const Plan& p, void* part, TileArgs& a) {
+  a.splits = (uint32_t)p.splits;
+  a.chunk = p.chunk;
+  a.part = p.splits > 1 ? (float*)part : nullptr;
+}
+
+// The backward pass's workspace: dp where it differs from dout, the bias's
+// partial sums, one row for each run of rows, and the splits' sums.
 struct BackPlan {
-  int64_t ld_dp, dp_bytes, run, runs, part_bytes;
+  int64_t ld_dp, dp_bytes, run, runs, bias_bytes, split_bytes;
+  int64_t bytes() const { return dp_bytes + bias_bytes + split_bytes; }
 };
 
 BackPlan plan_back(const echo_linear_desc* d, const Geometry& g) {
@@ -158,16 +247,10 @@ BackPlan plan_back(const echo_linear_desc* d, const Geometry& g) {
   b.run = round_up((g.m + most - 1) / most, 8);
   if (b.run < 32) b.run = 32;
   b.runs = (g.m + b.run - 1) / b.run;
-  b.part_bytes = round_up(b.runs * g.rows * 4, 16);
+  b.bias_bytes = round_up(b.runs * g.rows * 4, 16);
+  const int64_t dx = part_bytes(g.m, g.k, g.rows), dw = part_bytes(g.rows, g.k, g.m);
+  b.split_bytes = dx > dw ? dx : dw;  // one after the other on the stream
   return b;
-}
-
-int edge_of(int64_t I, int64_t cols) {
-  // a larger tile reads less per output; a smaller one fills the 256 compute
-  // units where there are few tiles
-  for (int edge = 256; edge > 64; edge /= 2)
-    if (((I + edge - 1) / edge) * ((cols + edge - 1) / edge) >= 192) return edge;
-  return 64;
 }
 
 }  // namespace
@@ -177,7 +260,7 @@ extern "C" {
 int64_t echo_linear_workspace(const echo_linear_desc* d) {
   Geometry g;
   const int rc = check_desc(d, g);
-  return rc ? rc : 0;
+  return rc ? rc : part_bytes(g.m, g.rows, g.k);
 }
 
 int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const void* bias,
@@ -188,9 +271,16 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
   if (rc) return rc;
   if (g.m == 0 || g.n == 0) return ECHO_SUCCESS;
   if (!out || (g.k > 0 && (!x || !w))) return ECHO_ERR_INVALID_ARGUMENT;
+  const int64_t need = part_bytes(g.m, g.rows, g.k);
+  if (need > 0) {
+    if (!workspace) return ECHO_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return ECHO_ERR_WORKSPACE;
+  }
   for (const void* q : {x, w, bias, residual, (const void*)out, (const void*)p})
     if (!aligned(q, 2)) return ECHO_ERR_ALIGNMENT;
+  if (!aligned(workspace, 16)) return ECHO_ERR_ALIGNMENT;
   Aliases al;
+  al.out(workspace, need);
   al.out(out, span(g.m, g.n, g.ld_out));
   al.out(p, g.m * g.rows * 2);
   al.in(x, span(g.m, g.k, g.ld_x));
@@ -207,8 +297,6 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
   a.I = g.m;
   a.J = g.n;
   a.C = g.k;
-  a.chunk = round_up(g.k, kC);
-  a.splits = 1;
   a.out = out;
   a.ldo = g.ld_out;
   a.p = p;
@@ -216,7 +304,12 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
   a.residual = residual;
   a.ldr = g.ld_r;
   a.act = d->act;
-  return tile_forward(a, d->dtype, d->gated != 0, edge_of(g.m, g.rows), (hipStream_t)stream);
+  const Plan plan = plan_tiles(g.m, g.rows, g.k, chunked<false, false>(a));
+  apply(plan, workspace, a);
+  const hipStream_t s = (hipStream_t)stream;
+  rc = tile_forward(a, d->dtype, d->gated != 0, plan.tile, s);
+  if (rc || plan.splits == 1) return rc;
+  return d->gated ? run_join<true>(a, d->dtype, s) : run_join<false>(a, d->dtype, s);
 }
 
 int64_t echo_linear_backward_workspace(const echo_linear_desc* d) {
@@ -224,7 +317,7 @@ int64_t echo_linear_backward_workspace(const echo_linear_desc* d) {
   const int rc = check_desc(d, g);
   if (rc) return rc;
   const BackPlan b = plan_back(d, g);
-  return b.dp_bytes + b.part_bytes;
+  return b.bytes();
 }
 
 int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void* x,
@@ -240,7 +333,7 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
     if (g.k > 0 && ((dx && !w) || (dw && !x))) return ECHO_ERR_INVALID_ARGUMENT;
   }
   const BackPlan b = plan_back(d, g);
-  const int64_t need = b.dp_bytes + b.part_bytes;
+  const int64_t need = b.bytes();
   if (need > 0) {
     if (!workspace) return ECHO_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return ECHO_ERR_WORKSPACE;
@@ -289,17 +382,19 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
   TileArgs a = {};
   a.a = slope ? workspace : dout;
   a.lda = slope ? b.ld_dp : g.ld_out;
-  a.splits = 1;
+  void* const splits = (char*)workspace + b.dp_bytes + b.bias_bytes;
   if (dx) {
     a.b = w;
     a.ldb = g.ld_w;
     a.I = g.m;
     a.J = g.k;
     a.C = g.rows;
-    a.chunk = round_up(a.C, kC);
     a.out = dx;
     a.ldo = g.k;
-    rc = tile_dx(a, d->dtype, edge_of(a.I, a.J), s);
+    const Plan plan = plan_tiles(a.I, a.J, a.C, chunked<false, true>(a));
+    apply(plan, splits, a);
+    rc = tile_dx(a, d->dtype, plan.tile, s);
+    if (!rc && plan.splits > 1) rc = run_join<false>(a, d->dtype, s);
     if (rc) return rc;
   }
   if (dw) {
@@ -308,10 +403,12 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
     a.I = g.rows;
     a.J = g.k;
     a.C = g.m;
-    a.chunk = round_up(a.C, kC);
     a.out = dw;
     a.ldo = g.k;
-    rc = tile_dw(a, d->dtype, edge_of(a.I, a.J), s);
+    const Plan plan = plan_tiles(a.I, a.J, a.C, chunked<true, true>(a));
+    apply(plan, splits, a);
+    rc = tile_dw(a, d->dtype, plan.tile, s);
+    if (!rc && plan.splits > 1) rc = run_join<false>(a, d->dtype, s);
   }
   return rc;
 }

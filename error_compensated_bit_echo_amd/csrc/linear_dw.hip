@@ -4,18 +4,21 @@
 namespace echo {
 
 template <typename T>
-static int product(const TileArgs& a, int edge, hipStream_t s) {
+static int product(const TileArgs& a, int tile, hipStream_t s) {
   if (chunked<true, true>(a)) {
-    if (edge == 256) return launch_tile<T, true, true, 256, 256, 2, 4, false, true>(a, s);
-    if (edge == 128) return launch_tile<T, true, true, 128, 128, 2, 2, false, true>(a, s);
-    return launch_tile<T, true, true, 64, 64, 2, 2, false, true>(a, s);
+    switch (tile) {
+      case kTile256: return launch_tile<T, true, true, 256, 256, 2, 4, false, 2>(a, s);
+      case kTile256x128: return launch_tile<T, true, true, 256, 128, 4, 2, false, 3>(a, s);
+      case kTile128: return launch_tile<T, true, true, 128, 128, 2, 2, false, 2>(a, s);
+      default: return launch_tile<T, true, true, 64, 64, 2, 2, false, 4>(a, s);
+    }
   }
-  if (edge >= 128) return launch_tile<T, true, true, 128, 128, 2, 2, false, false>(a, s);
-  return launch_tile<T, true, true, 64, 64, 2, 2, false, false>(a, s);
+  if (tile != kTile64) return launch_tile<T, true, true, 128, 128, 2, 2, false, 0>(a, s);
+  return launch_tile<T, true, true, 64, 64, 2, 2, false, 0>(a, s);
 }
 
-int tile_dw(const TileArgs& a, int32_t dtype, int edge, hipStream_t s) {
-  return dtype == ECHO_BF16 ? product<bf16_t>(a, edge, s) : product<f16_t>(a, edge, s);
+int tile_dw(const TileArgs& a, int32_t dtype, int tile, hipStream_t s) {
+  return dtype == ECHO_BF16 ? product<bf16_t>(a, tile, s) : product<f16_t>(a, tile, s);
 }
 
 }  // namespace echo

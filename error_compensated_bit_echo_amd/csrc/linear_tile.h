@@ -21,6 +21,18 @@ __device__ __forceinline__ u32x4 raw8(const T* p, int64_t n) {
   return w;
 }
 
+template <int W>
+__device__ __forceinline__ void store_sums(float* p, int n, const float (&v)[W]) {
+  if (n >= W) {
+#pragma unroll
+    for (int e = 0; e < W; e += 4) *(f32x4_a4*)(p + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+
 // A wavefront's sums to the epilogue, or to a split's partial sums.  Lane
 // 16 g + rho holds row rho of each of A's fragments; along j it holds four sums
 // of one fragment of B or, paired, eight of two.
@@ -47,12 +59,8 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const f32x4 (&acc)
       const int n = (int)min(a.J - col, (int64_t)W);
       if (a.splits > 1) {
         float* p = a.part + ((int64_t)split * a.I + row) * cols + col;
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (e < n) {
-            p[e] = v[e];
-            if (GATED) p[a.J + e] = u[e];
-          }
+        store_sums<W>(p, n, v);
+        if (GATED) store_sums<W>(p + a.J, n, u);
       } else {
         finish<T, W, GATED>(a, row, col, n, v, u);
       }
@@ -167,8 +175,12 @@ __device__ __forceinline__ void dma16(u32x4 range, lds_short* lds, int offset) {
       : "memory");
 }
 
-// wait until this wavefront's chunks have arrived in LDS
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// wait until at most LEFT of this wavefront's loads are still on their way;
+// they arrive in the order of their issue
+template <int LEFT>
+__device__ __forceinline__ void dma_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LEFT) : "memory");
+}
 
 // descriptor of `bytes` bytes from p on, unformatted, checked byte by byte
 __device__ __forceinline__ u32x4 range_of(const void* p, int64_t bytes) {
@@ -177,9 +189,12 @@ __device__ __forceinline__ u32x4 range_of(const void* p, int64_t bytes) {
 }
 
 // The same tile fed by direct loads into LDS, for operands whose 16-byte chunks
-// are aligned and, along c, whole.  While one stage is multiplied the next one
-// arrives; no register holds a chunk on its way.
-template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED>
+// are aligned and, along c, whole; no register holds a chunk on its way.  S
+// stages are on their way or in use: while one is multiplied the S - 1 after it
+// arrive.  A step waits for its own stage only, and its one barrier says both
+// that every wavefront's part of the stage is there and that the stage before,
+// whose place the next loads take, has been read.
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S>
 __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr bool PAIRED = !TB;
@@ -187,7 +202,10 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   static_assert(!PAIRED || TJ % (GATED ? 4 : 2) == 0, "fragments of a wavefront");
   typedef OperandTile<TA, false, BI, NT> A;
   typedef OperandTile<TB, PAIRED, BJ, NT> B;
-  __shared__ short lds0[(BI + BJ) * kC], lds1[(BI + BJ) * kC];
+  constexpr int kStage = (BI + BJ) * kC, kLoads = A::kPer + B::kPer;
+  static_assert((S - 1) * kLoads < 64, "loads in flight");
+  __shared__ short lds_mem[S * kStage];
+  lds_short* const lds = (lds_short*)lds_mem;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -221,7 +239,8 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   const T* pa = (const T*)a.a + (TA ? c0 * a.lda + i0 : i0 * a.lda + c0);
   const T* pb = (const T*)a.b + (TB ? c0 * a.ldb + j0 : j0 * a.ldb + c0);
   constexpr int kPast = 0x7FFFFFF0;  // an offset past every range
-  auto stage = [&](lds_short* lds, int s) {
+  // past the last step the ranges are empty, so every step issues as many loads
+  auto stage = [&](lds_short* la, int s) {
     const int64_t left = c1 - c0 - (int64_t)s * kC;  // of the contraction, from this step on
     const bool tail = left < kC;
     if constexpr (TA) {
@@ -229,16 +248,16 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
       const auto r = range_of(pa + (int64_t)s * kC * a.lda,
                               (((min(left, (int64_t)kC) - 1) * a.lda + (a.I - i0)) * 2 + 2) & ~(int64_t)3);
 #pragma unroll
-      for (int i = 0; i < A::kPer; ++i) dma16(r, lds + (i * NT + wave * 64) * 8, oa[i]);
+      for (int i = 0; i < A::kPer; ++i) dma16(r, la + (i * NT + wave * 64) * 8, oa[i]);
     } else {
       const auto r = range_of(pa, ((rows_a - 1) * a.lda + (c1 - c0)) * 2);
 #pragma unroll
       for (int i = 0; i < A::kPer; ++i) {
         const int o = oa[i] + s * kC * 2;
-        dma16(r, lds + (i * NT + wave * 64) * 8, tail && ca[i] >= left ? kPast : o);
+        dma16(r, la + (i * NT + wave * 64) * 8, tail && ca[i] >= left ? kPast : o);
       }
     }
-    lds_short* lb = lds + BI * kC;
+    lds_short* lb = la + BI * kC;
     if constexpr (TB) {
       const auto r = range_of(pb + (int64_t)s * kC * a.ldb,
                               (((min(left, (int64_t)kC) - 1) * a.ldb + (a.J - j0)) * 2 + 2) & ~(int64_t)3);
@@ -279,21 +298,20 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
     }
   };
 
-  if (steps > 0) stage((lds_short*)lds0, 0);
-  dma_wait();
-  __syncthreads();
-  for (int s = 0; s < steps; s += 2) {
-    if (s + 1 < steps) stage((lds_short*)lds1, s + 1);
-    multiply((lds_short*)lds0);
-    dma_wait();
-    __syncthreads();
-    if (s + 1 < steps) {
-      if (s + 2 < steps) stage((lds_short*)lds0, s + 2);
-      multiply((lds_short*)lds1);
-      dma_wait();
-      __syncthreads();
+#pragma unroll
+  for (int u = 0; u < S - 1; ++u) stage(lds + u * kStage, u);
+  for (int s = 0; s < steps; s += S) {
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      if (s + u < steps) {
+        dma_wait<(S - 2) * kLoads>();
+        __syncthreads();
+        stage(lds + (u + S - 1) % S * kStage, s + u + S - 1);
+        multiply(lds + u * kStage);
+      }
     }
   }
+  dma_wait<0>();  // nothing may arrive in LDS after the workgroup has left it
   write_tile<T, PAIRED, GATED, TI, TJ>(a, acc, i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
@@ -304,7 +322,8 @@ bool chunked(const TileArgs& a) {
          ((TA && TB) || a.C % 8 == 0);
 }
 
-template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, bool DMA>
+// S: stages fed by direct loads, or 0 for the kernel that stages through registers
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S>
 int launch_tile(TileArgs a, hipStream_t s) {
   const int64_t out = GATED ? BJ / 2 : BJ;
   const int64_t ti = (a.I + BI - 1) / BI, tj = (a.J + out - 1) / out;
@@ -314,15 +333,19 @@ int launch_tile(TileArgs a, hipStream_t s) {
   a.tiles_i = (uint32_t)ti;
   a.tiles_j = (uint32_t)tj;
   const dim3 grid(a.tiles_i * a.tiles_j * a.splits);
-  if constexpr (DMA) return launch(k_tile_dma<T, TA, TB, BI, BJ, WI, WJ, GATED>, grid, dim3(NT), s, a);
+  if constexpr (S > 0) return launch(k_tile_dma<T, TA, TB, BI, BJ, WI, WJ, GATED, S>, grid, dim3(NT), s, a);
   else return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED>, grid, dim3(NT), s, a);
 }
 
 }  // namespace
 
-// The products, by the tile's edge (128 or 64), one source file each.
-int tile_forward(const TileArgs& a, int32_t dtype, bool gated, int edge, hipStream_t s);
-int tile_dx(const TileArgs& a, int32_t dtype, int edge, hipStream_t s);
-int tile_dw(const TileArgs& a, int32_t dtype, int edge, hipStream_t s);
+// Tiles, largest first; operands that are not chunked take kTile128 or kTile64
+// through registers.
+enum TileKind { kTile256 = 0, kTile256x128 = 1, kTile128 = 2, kTile64 = 3, kTileKinds = 4 };
+
+// The products, one source file each.
+int tile_forward(const TileArgs& a, int32_t dtype, bool gated, int tile, hipStream_t s);
+int tile_dx(const TileArgs& a, int32_t dtype, int tile, hipStream_t s);
+int tile_dw(const TileArgs& a, int32_t dtype, int tile, hipStream_t s);
 
 }  // namespace echo
