@@ -14,6 +14,7 @@ missing the import fails loudly.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 
 import torch  # load torch's HIP runtime first: libecho binds to the same one
@@ -162,8 +163,8 @@ def _ptrs(ts, nbytes: int = 0, what: str = "buffers"):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # torch's current stream, without building a Stream object (2.7 us of a 12 us call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -423,43 +424,48 @@ def _code(table, key, what):
     return table[key]
 
 
-def _tensor(t, dtype, what):
+def _bad_tensor(t, shape, dtype, what):
+    """what is wrong with a tensor that its call cannot take"""
     if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{what}: a tensor is required")
+        return f"{what}: a tensor is required"
     if not t.is_cuda:
-        raise ValueError(f"{what}: a GPU tensor is required (got one on {t.device})")
+        return f"{what}: a GPU tensor is required (got one on {t.device})"
     if t.dtype != dtype:
-        raise ValueError(f"{what}: {dtype} is required (got {t.dtype})")
+        return f"{what}: {dtype} is required (got {t.dtype})"
+    if t.dim() == 0 or t.shape[-1] != shape[-1] or t.numel() != math.prod(shape):
+        return f"{what}: shape {tuple(t.shape)}, the call needs {tuple(shape)}"
+    return None
 
 
 def _matrix(t, rows, cols, dtype, what):
     """(address, row pitch in elements) of a [rows, cols] matrix with unit
     stride along its rows, or of a dense tensor of any shape whose last
     dimension is cols."""
-    _tensor(t, dtype, what)
-    if t.dim() == 0 or t.shape[-1] != cols or t.numel() != rows * cols:
-        raise ValueError(f"{what}: shape {tuple(t.shape)} does not hold {rows} rows of {cols}")
-    if t.is_contiguous():
-        return t.data_ptr(), cols
-    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
-        raise ValueError(f"{what}: rows of unit stride that do not overlap are required "
-                         f"(strides {t.stride()})")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype:
+        shape = t.shape
+        if shape and shape[-1] == cols and t.numel() == rows * cols:
+            if t.is_contiguous():
+                return t.data_ptr(), cols
+            if len(shape) == 2:
+                stride = t.stride()
+                if (cols <= 1 or stride[1] == 1) and (rows <= 1 or stride[0] >= cols):
+                    return t.data_ptr(), (stride[0] if rows > 1 else cols)
+    bad = _bad_tensor(t, (rows, cols), dtype, what)
+    raise ValueError(bad or f"{what}: rows of unit stride that do not overlap are required (strides {t.stride()})")
 
 
 def _dense(t, shape, dtype, what):
-    """address of a dense tensor of as many elements as `shape` has (None -> NULL)"""
+    """address of a dense tensor of this shape, or of any whose last dimension
+    and number of elements are the same (None -> NULL)"""
     if t is None:
         return None
-    _tensor(t, dtype, what)
-    n = 1
-    for s in shape:
-        n *= s
-    if t.numel() != n or (len(shape) > 1 and n and t.shape[-1] != shape[-1]):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: the tensor must be contiguous")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype:
+        have = t.shape
+        if have == shape or (have and have[-1] == shape[-1] and t.numel() == math.prod(shape)):
+            if t.is_contiguous():
+                return t.data_ptr()
+    bad = _bad_tensor(t, shape, dtype, what)
+    raise ValueError(bad or f"{what}: the tensor must be contiguous")
 
 
 def _workspace(t):
@@ -469,11 +475,20 @@ def _workspace(t):
     return _ptr(t, 0, "workspace"), t.nbytes
 
 
+def _dtype_of(t, what):
+    if not isinstance(t, torch.Tensor) or t.dtype not in DTYPES:
+        raise ValueError(f"{what}: a bfloat16, float16 or float32 tensor is required")
+    return t.dtype
+
+
 def _rows_of(t, what):
-    if not isinstance(t, torch.Tensor) or t.dim() == 0 or t.dtype not in DTYPES:
-        raise ValueError(f"{what}: a bfloat16, float16 or float32 tensor with rows is required")
-    cols = t.shape[-1]
-    return (t.numel() // cols if cols else 0), cols
+    """(rows, columns) of a tensor whose last dimension is a row"""
+    _dtype_of(t, what)
+    shape = t.shape
+    if not shape:
+        raise ValueError(f"{what}: a tensor with rows is required")
+    cols = shape[-1]
+    return (t.numel() // cols if cols else math.prod(shape[:-1])), cols
 
 
 def _same_pitch(a, b, what):
@@ -492,10 +507,7 @@ def echo_norm(h, y, h_out, z, *, post="none", w_post=None, b_post=None, gate=Non
     pass follows.  post and pre are "none", "rms" or "layer".  y, h_out and z
     may be None as include/echo_layer.h says; h_out may be h."""
     T, H = _rows_of(h, "h")
-    first = next((t for t in (y, z, w_pre) if t is not None), h)
-    if not isinstance(first, torch.Tensor) or first.dtype not in DTYPES:
-        raise ValueError("y, z: a bfloat16, float16 or float32 tensor is required")
-    dt, sdt = first.dtype, h.dtype
+    dt, sdt = _dtype_of(h if y is None and z is None else z if y is None else y, "y, z"), h.dtype
     hp, ldh = _matrix(h, T, H, sdt, "h")
     yp, ldy = _matrix(y, T, H, dt, "y") if y is not None else (None, 0)
     op, ldo = _matrix(h_out, T, H, sdt, "h_out") if h_out is not None else (None, None)
@@ -525,10 +537,8 @@ def echo_norm_backward(dz, dh_out, h_out, y, stats, dh, dy, *, post="none", w_po
     h_out and stats.  The parameters are those of the forward call; workspace
     is needed where a parameter's gradient is wanted."""
     T, H = _rows_of(dh, "dh")
-    first = next((t for t in (dz, dy, y) if t is not None), dh)
-    if not isinstance(first, torch.Tensor) or first.dtype not in DTYPES:
-        raise ValueError("dz, dy, y: a bfloat16, float16 or float32 tensor is required")
-    dt, sdt = first.dtype, dh.dtype
+    some = dz if dz is not None else dy if dy is not None else y if y is not None else dh
+    dt, sdt = _dtype_of(some, "dz, dy, y"), dh.dtype
     hp, ldh = _matrix(h_out, T, H, sdt, "h_out") if h_out is not None else (None, 0)
     yp, ldy = _matrix(y, T, H, dt, "y") if y is not None else (None, 0)
     G = 0 if gate is None else _rows_of(gate, "gate")[0]
@@ -565,11 +575,14 @@ def echo_linear_backward_workspace(m, n, k, act="none", gated=False) -> int:
 
 
 def _linear_shape(x, w, gated):
-    m, k = _rows_of(x, "x") if x.shape[-1] else (x.numel() if x.dim() < 2 else x.shape[:-1].numel(), 0)
-    rows = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 2 else -1
-    if rows < 0 or (gated and rows % 2):
+    """(m, n, k, rows of w, type)"""
+    m, k = _rows_of(x, "x")
+    if x.dtype is torch.float32:
+        raise ValueError("x: a bfloat16 or float16 tensor is required")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or (gated and w.shape[0] % 2):
         raise ValueError("w: a matrix is required, with an even number of rows if the product is gated")
-    return m, (rows // 2 if gated else rows), k, rows
+    rows = w.shape[0]
+    return m, (rows // 2 if gated else rows), k, rows, x.dtype
 
 
 def echo_linear(x, w, out, *, bias=None, residual=None, act="none", gated=False, p=None, workspace=None,
@@ -581,10 +594,7 @@ def echo_linear(x, w, out, *, bias=None, residual=None, act="none", gated=False,
     (dense, kept for the backward call) as wide as w has rows; all bfloat16 or
     all float16.  act is "none", "relu", "gelu", "gelu_tanh" or "silu".  out may
     be residual."""
-    if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("x: a bfloat16 or float16 tensor with rows is required")
-    m, n, k, rows = _linear_shape(x, w, gated)
-    dt = x.dtype
+    m, n, k, rows, dt = _linear_shape(x, w, gated)
     xp, ldx = _matrix(x, m, k, dt, "x")
     wp, ldw = _matrix(w, rows, k, dt, "w")
     op, ldo = _matrix(out, m, n, dt, "out")
@@ -600,10 +610,7 @@ def echo_linear_backward(dout, x, w, p, dx, dw, *, dbias=None, act="none", gated
     """Gradients of echo_linear: dx, dw and dbias, each None to skip it, from
     dout and the forward call's x, w and p (p may be None without an activation
     and a gate).  The residual's gradient is dout."""
-    if not isinstance(x, torch.Tensor) or x.dim() == 0 or x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("x: a bfloat16 or float16 tensor with rows is required")
-    m, n, k, rows = _linear_shape(x, w, gated)
-    dt = x.dtype
+    m, n, k, rows, dt = _linear_shape(x, w, gated)
     gp, ldo = _matrix(dout, m, n, dt, "dout")
     xp, ldx = _matrix(x, m, k, dt, "x")
     wp, ldw = _matrix(w, rows, k, dt, "w")
