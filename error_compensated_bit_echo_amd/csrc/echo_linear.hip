@@ -215,6 +215,10 @@ int64_t part_bytes(int64_t I, int64_t cols, int64_t C) {
   return round_up(a > b ? a : b, 16);
 }
 
+int64_t forward_bytes(const Geometry& g) {
+  return g.m <= kFewRows ? 0 : part_bytes(g.m, g.rows, g.k);
+}
+
 template <bool GATED>
 int run_join(const TileArgs& a, int32_t dtype, hipStream_t s) {
   const uint64_t items = (uint64_t)a.I * (uint64_t)((a.J + 7) / 8);
@@ -260,7 +264,7 @@ extern "C" {
 int64_t echo_linear_workspace(const echo_linear_desc* d) {
   Geometry g;
   const int rc = check_desc(d, g);
-  return rc ? rc : part_bytes(g.m, g.rows, g.k);
+  return rc ? rc : forward_bytes(g);
 }
 
 int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const void* bias,
@@ -271,7 +275,7 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
   if (rc) return rc;
   if (g.m == 0 || g.n == 0) return ECHO_SUCCESS;
   if (!out || (g.k > 0 && (!x || !w))) return ECHO_ERR_INVALID_ARGUMENT;
-  const int64_t need = part_bytes(g.m, g.rows, g.k);
+  const int64_t need = forward_bytes(g);
   if (need > 0) {
     if (!workspace) return ECHO_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return ECHO_ERR_WORKSPACE;
@@ -304,9 +308,10 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
   a.residual = residual;
   a.ldr = g.ld_r;
   a.act = d->act;
+  const hipStream_t s = (hipStream_t)stream;
+  if (g.m <= kFewRows) return rows_forward(a, d->dtype, d->gated != 0, s);
   const Plan plan = plan_tiles(g.m, g.rows, g.k, chunked<false, false>(a));
   apply(plan, workspace, a);
-  const hipStream_t s = (hipStream_t)stream;
   rc = tile_forward(a, d->dtype, d->gated != 0, plan.tile, s);
   if (rc || plan.splits == 1) return rc;
   return d->gated ? run_join<true>(a, d->dtype, s) : run_join<false>(a, d->dtype, s);
