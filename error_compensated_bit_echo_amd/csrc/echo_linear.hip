@@ -21,8 +21,9 @@ namespace {
 // down the rows of its workgroup's run; 32 threads lie side by side, 8 above
 // each other.  Bound by HBM: 2 bytes in per dout and p element, 2 out.
 struct SlopeArgs {
-  const void *dout, *p;
-  void* dp;     // nullable: dp is dout itself
+  const void *dout;
+  const void* p;  // nullable: no activation, dp is a copy of dout
+  void* dp;       // nullable: dp is dout itself; rows filled up with zeros to ld_dp
   float* part;  // nullable: [runs][columns of dp] sums
   int64_t m, n, ld_out, ld_dp, run;
   int32_t act, gated;
@@ -34,7 +35,7 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 256 + tx * 8;
   const int64_t r0 = (int64_t)blockIdx.y * a.run, r1 = min(r0 + a.run, a.m);
-  const int n = (int)min(a.n - col, (int64_t)8);
+  const int n = (int)min(a.n - col, (int64_t)9);  // 8 or less: the row's last vector
   const int64_t cols = a.gated ? 2 * a.n : a.n;
   float sg[8], su[8];
 #pragma unroll
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
     for (int64_t r = r0 + ty; r < r1; r += 8) {
       float d[8], p[8], u[8];
       load_n<false>((const T*)a.dout + r * a.ld_out + col, n, d);
-      if (a.dp) {
+      if (a.p) {
         load_n<true>((const T*)a.p + r * cols + col, n, p);
         if (a.gated) load_n<true>((const T*)a.p + r * cols + a.n + col, n, u);
 #pragma unroll
@@ -56,8 +57,13 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
           }
           d[e] *= slope;
         }
-        store_n<false>((T*)a.dp + r * a.ld_dp + col, n, d);
-        if (a.gated) store_n<false>((T*)a.dp + r * a.ld_dp + a.n + col, n, p);
+      }
+      if (a.dp) {
+        T* dp = (T*)a.dp + r * a.ld_dp;
+        store_n<false>(dp + col, n, d);
+        if (a.gated) store_n<false>(dp + a.n + col, n, p);
+        if (n <= 8)
+          for (int64_t c = cols; c < a.ld_dp; ++c) dp[c] = from_f32<T>(0.f);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -80,6 +86,32 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
       for (int k = 1; k < 8; ++k) s += lds[h][k][threadIdx.x];
       a.part[(int64_t)blockIdx.y * cols + h * a.n + c] = s;
     }
+}
+
+// ---- rows of odd lengths ------------------------------------------------------------
+// Copies of up to two operands whose rows are no whole number of 16-byte chunks,
+// each row filled up with zeros, for the tiles fed by direct loads: the copy
+// moves each operand twice, the tiles save a third of the product's time.
+struct PackArgs {
+  const void* src[2];
+  void* dst[2];
+  int64_t rows[2], ld[2];
+  int64_t cols, pitch;  // pitch: cols rounded up to 8
+};
+
+// a wavefront to a row
+template <typename T>
+__global__ __launch_bounds__(kBlock) void k_pack(PackArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = a.rows[0] + a.rows[1];
+  for (int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6); t < rows;
+       t += (int64_t)gridDim.x * kWavesPerBlock) {
+    const int k = t >= a.rows[0];
+    const int64_t r = k ? t - a.rows[0] : t;
+    const T* src = (const T*)a.src[k] + r * a.ld[k];
+    T* dst = (T*)a.dst[k] + r * a.pitch;
+    for (int64_t c = lane * 8; c < a.pitch; c += 512) *(u32x4*)(dst + c) = raw8(src + c, a.cols - c);
+  }
 }
 
 // out[c] = sum over the runs of part[run][c], in a fixed order
@@ -179,15 +211,14 @@ struct TileCost { int bi, bj; float step, alone; };
 constexpr TileCost kChunkedCost[kTileKinds] = {
     {256, 256, 1.65f, 1.65f}, {256, 128, 1.00f, 1.00f}, {128, 128, 0.50f, 0.62f}, {64, 64, 0.18f, 0.22f}};
 constexpr TileCost kStagedCost[kTileKinds] = {
-    {0, 0, 0, 0}, {0, 0, 0, 0}, {128, 128, 0.67f, 0.85f}, {64, 64, 0.23f, 0.50f}};
+    {0, 0, 0, 0}, {0, 0, 0, 0}, {128, 128, 1.00f, 1.10f}, {64, 64, 0.38f, 0.50f}};
 constexpr int64_t kMostPart = INT64_C(256) << 20;  // bytes of partial sums
 
-struct Plan { int tile; int64_t splits, chunk, part_bytes; };
+struct Plan { int tile; int64_t splits, chunk, part_bytes; double us; };
 
 Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
   const int64_t steps = (C + kC - 1) / kC;
-  Plan best = {kTile64, 1, steps * kC, 0};
-  double least = 1e30;
+  Plan best = {kTile64, 1, steps * kC, 0, 1e30};
   for (int t = 0; t < kTileKinds; ++t) {
     const TileCost& k = is_chunked ? kChunkedCost[t] : kStagedCost[t];
     if (k.bi == 0) continue;
@@ -200,10 +231,7 @@ Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
       const double per_cu = ceil(tiles * (double)splits / 256.0);
       const double busy = per_cu * k.step > k.alone ? per_cu * k.step : k.alone;
       const double us = (double)each * busy + (splits > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
-      if (us < least) {
-        least = us;
-        best = {t, splits, each * kC, splits > 1 ? (int64_t)bytes : 0};
-      }
+      if (us < best.us) best = {t, splits, each * kC, splits > 1 ? (int64_t)bytes : 0, us};
     }
   }
   return best;
@@ -215,8 +243,41 @@ int64_t part_bytes(int64_t I, int64_t cols, int64_t C) {
   return round_up(a > b ? a : b, 16);
 }
 
+// Rows of odd lengths.  Their chunks are neither aligned nor whole, so either
+// the tiles stage them through registers, or copies with whole rows are made
+// first (one launch, and every copied byte read and written) for the tiles fed
+// by direct loads; the estimates decide.
+int64_t copy_bytes(int64_t rows, int64_t cols) { return round_up(rows * round_up(cols, 8) * 2, 16); }
+double copy_us(int64_t bytes) { return 3.5 + (double)bytes * 2.0 / 4.5e6; }
+
+bool copy_forward(const Geometry& g) {
+  return g.k % 8 != 0 && plan_tiles(g.m, g.rows, g.k, true).us + copy_us(copy_bytes(g.m + g.rows, g.k)) <
+                             plan_tiles(g.m, g.rows, g.k, false).us;
+}
+
+int run_pack(const Geometry& g, const void* x, void* px, const void* w, void* pw, int32_t dtype,
+             hipStream_t s) {
+  PackArgs a = {};
+  a.src[0] = x;
+  a.dst[0] = px;
+  a.rows[0] = x ? g.m : 0;
+  a.ld[0] = g.ld_x;
+  a.src[1] = w;
+  a.dst[1] = pw;
+  a.rows[1] = w ? g.rows : 0;
+  a.ld[1] = g.ld_w;
+  a.cols = g.k;
+  a.pitch = round_up(g.k, 8);
+  const uint64_t rows = (uint64_t)(a.rows[0] + a.rows[1]);
+  if (rows == 0 || a.cols == 0) return ECHO_SUCCESS;
+  const dim3 grid(blocks_for(rows)), block(kBlock);
+  return dtype == ECHO_BF16 ? launch(k_pack<bf16_t>, grid, block, s, a) : launch(k_pack<f16_t>, grid, block, s, a);
+}
+
 int64_t forward_bytes(const Geometry& g) {
-  return g.m <= kFewRows ? 0 : part_bytes(g.m, g.rows, g.k);
+  if (g.m <= kFewRows) return 0;
+  const int64_t copies = copy_forward(g) ? copy_bytes(g.m, g.k) + copy_bytes(g.rows, g.k) : 0;
+  return copies + part_bytes(g.m, g.rows, g.k);
 }
 
 template <bool GATED>
@@ -233,16 +294,31 @@ void apply(const Plan& p, void* part, TileArgs& a) {
   a.part = p.splits > 1 ? (float*)part : nullptr;
 }
 
-// The backward pass's workspace: dp where it differs from dout, the bias's
-// partial sums, one row for each run of rows, and the splits' sums.
+// The backward pass's workspace: dp where it differs from dout, copies of dout,
+// x and w with whole rows where those pay, the bias's partial sums, one row for
+// each run of rows, and the splits' sums.
 struct BackPlan {
-  int64_t ld_dp, dp_bytes, run, runs, bias_bytes, split_bytes;
-  int64_t bytes() const { return dp_bytes + bias_bytes + split_bytes; }
+  bool copies;
+  int64_t ld_dp, dp_bytes, x_bytes, w_bytes, run, runs, bias_bytes, split_bytes;
+  int64_t bytes() const { return dp_bytes + x_bytes + w_bytes + bias_bytes + split_bytes; }
 };
 
 BackPlan plan_back(const echo_linear_desc* d, const Geometry& g) {
   BackPlan b = {};
-  if (d->act != ECHO_ACT_NONE || d->gated) {
+  const bool slope = d->act != ECHO_ACT_NONE || d->gated;
+  const bool odd_k = g.k % 8 != 0, odd_n = !slope && g.n % 8 != 0;
+  if (odd_k || odd_n) {
+    const double copied = plan_tiles(g.m, g.k, g.rows, true).us + plan_tiles(g.rows, g.k, g.m, true).us;
+    const double staged = plan_tiles(g.m, g.k, g.rows, false).us + plan_tiles(g.rows, g.k, g.m, false).us;
+    const double cost = (odd_k ? copy_us(copy_bytes(g.m + g.rows, g.k)) : 0.0) +
+                        (odd_n ? copy_us(copy_bytes(g.m, g.n)) : 0.0);
+    b.copies = copied + cost < staged;
+  }
+  if (b.copies && odd_k) {
+    b.x_bytes = copy_bytes(g.m, g.k);
+    b.w_bytes = copy_bytes(g.rows, g.k);
+  }
+  if (slope || (b.copies && odd_n)) {
     b.ld_dp = round_up(g.rows, 8);
     b.dp_bytes = round_up(g.m * b.ld_dp * 2, 16);
   }
@@ -310,8 +386,19 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
   a.act = d->act;
   const hipStream_t s = (hipStream_t)stream;
   if (g.m <= kFewRows) return rows_forward(a, d->dtype, d->gated != 0, s);
+  char* ws = (char*)workspace;
+  if (copy_forward(g)) {
+    char* pw = ws + copy_bytes(g.m, g.k);
+    rc = run_pack(g, x, ws, w, pw, d->dtype, s);
+    if (rc) return rc;
+    a.a = ws;
+    a.b = pw;
+    a.lda = a.ldb = round_up(g.k, 8);
+    a.padded = 1;
+    ws = pw + copy_bytes(g.rows, g.k);
+  }
   const Plan plan = plan_tiles(g.m, g.rows, g.k, chunked<false, false>(a));
-  apply(plan, workspace, a);
+  apply(plan, ws, a);
   rc = tile_forward(a, d->dtype, d->gated != 0, plan.tile, s);
   if (rc || plan.splits == 1) return rc;
   return d->gated ? run_join<true>(a, d->dtype, s) : run_join<false>(a, d->dtype, s);
@@ -359,13 +446,16 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
 
   const hipStream_t s = (hipStream_t)stream;
   const bool bf16 = d->dtype == ECHO_BF16;
-  float* part = (float*)((char*)workspace + b.dp_bytes);
-  const bool want_dp = slope && (dx || dw);
+  char* const px = (char*)workspace + b.dp_bytes;
+  char* const pw = px + b.x_bytes;
+  float* const part = (float*)(pw + b.w_bytes);
+  const bool own_dp = b.dp_bytes > 0, pack = b.x_bytes + b.w_bytes > 0;
+  const bool want_dp = own_dp && (dx || dw);
   if (some && (want_dp || dbias)) {
     SlopeArgs a = {};
     a.dout = dout;
-    a.p = p;
-    a.dp = slope ? workspace : nullptr;
+    a.p = slope ? p : nullptr;
+    a.dp = want_dp ? workspace : nullptr;
     a.part = dbias ? part : nullptr;
     a.m = g.m;
     a.n = g.n;
@@ -385,12 +475,17 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
     if (rc) return rc;
   }
   TileArgs a = {};
-  a.a = slope ? workspace : dout;
-  a.lda = slope ? b.ld_dp : g.ld_out;
-  void* const splits = (char*)workspace + b.dp_bytes + b.bias_bytes;
+  a.a = own_dp ? workspace : dout;
+  a.lda = own_dp ? b.ld_dp : g.ld_out;
+  a.padded = own_dp;
+  void* const splits = (char*)part + b.bias_bytes;
+  if (pack && some) {
+    rc = run_pack(g, dw ? x : nullptr, px, dx ? w : nullptr, pw, d->dtype, s);
+    if (rc) return rc;
+  }
   if (dx) {
-    a.b = w;
-    a.ldb = g.ld_w;
+    a.b = pack ? pw : w;
+    a.ldb = pack ? round_up(g.k, 8) : g.ld_w;
     a.I = g.m;
     a.J = g.k;
     a.C = g.rows;
@@ -403,8 +498,8 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
     if (rc) return rc;
   }
   if (dw) {
-    a.b = x;
-    a.ldb = g.ld_x;
+    a.b = pack ? px : x;
+    a.ldb = pack ? round_up(g.k, 8) : g.ld_x;
     a.I = g.rows;
     a.J = g.k;
     a.C = g.m;

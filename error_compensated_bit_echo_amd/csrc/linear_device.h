@@ -48,6 +48,7 @@ struct TileArgs {
   int64_t ldo, ldr;
   uint32_t tiles_i, tiles_j, splits;
   int32_t act;
+  int32_t padded;   // rows along c are followed by zeros up to a whole chunk
 };
 
 // ---- activations ---------------------------------------------------------------
@@ -204,19 +205,9 @@ struct OperandTile {
   }
 };
 
-// B's row for row r of its tile: gated, runs of 32 gate rows and the 32 up rows
-// of the same outputs alternate, so one lane holds both sums of an output.
-template <bool GATED>
-__device__ __forceinline__ void b_row(int r, int64_t j0, int64_t J, int64_t& row, bool& there) {
-  if (!GATED) {
-    row = j0 + r;
-    there = row < J;
-  } else {
-    const int64_t j = j0 + (r >> 6) * 32 + (r & 31);
-    there = j < J;
-    row = (r >> 5 & 1) ? J + j : j;
-  }
-}
+// Gated, B's tile alternates runs of 32 gate rows and the 32 up rows of the same
+// outputs, so one lane holds both sums of an output: row r of the tile belongs
+// to output (r / 64) 32 + r % 32, and bit 5 of r says up.
 
 // Workgroups are dealt to the 8 XCDs in turn; renumbered, an XCD takes one run
 // of tiles, and runs go over kBand tile rows before the next tile column, so

@@ -13,8 +13,8 @@ static int product(const TileArgs& a, int tile, hipStream_t s) {
       default: return launch_tile<T, false, true, 64, 64, 2, 2, false, 4>(a, s);
     }
   }
-  if (tile != kTile64) return launch_tile<T, false, true, 128, 128, 2, 2, false, 0>(a, s);
-  return launch_tile<T, false, true, 64, 64, 2, 2, false, 0>(a, s);
+  if (tile != kTile64) return launch_tile<T, false, true, 128, 128, 2, 2, false, -2>(a, s);
+  return launch_tile<T, false, true, 64, 64, 2, 2, false, -3>(a, s);
 }
 
 int tile_dx(const TileArgs& a, int32_t dtype, int tile, hipStream_t s) {

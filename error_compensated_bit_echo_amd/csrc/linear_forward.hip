@@ -14,8 +14,8 @@ static int forward(const TileArgs& a, int tile, hipStream_t s) {
       default: return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, 4>(a, s);
     }
   }
-  if (tile != kTile64) return launch_tile<T, false, false, 128, 128, 2, 2, GATED, 0>(a, s);
-  return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, 0>(a, s);
+  if (tile != kTile64) return launch_tile<T, false, false, 128, 128, 2, 2, GATED, -2>(a, s);
+  return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, -3>(a, s);
 }
 
 template <typename T>

@@ -68,7 +68,9 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const f32x4 (&acc)
   }
 }
 
-template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED>
+// Operands of any pitch and alignment: chunks go through registers, D steps
+// ahead of their use, since a step of a small tile is far shorter than a load.
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int D>
 __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr bool PAIRED = !TB;
@@ -89,38 +91,55 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
   const int steps = (int)((c1 - c0 + kC - 1) / kC);
 
-  u32x4 ra[A::kPer], rb[B::kPer];
-  auto load = [&](int64_t c) {
+  // The thread's chunks of step 0.  Rows past an operand's end repeat its last
+  // row: what they add up to is not written.
+  const T *pa[A::kPer], *pb[B::kPer];
+  int ca[A::kPer], cb[B::kPer];  // along c: the chunk's first element of the step; across: its row
 #pragma unroll
-    for (int i = 0; i < A::kPer; ++i) {
-      const int q = i * NT + tid, r = q / A::kRow, col = A::place(r, q % A::kRow) * 8;
-      if constexpr (TA) {
-        const int64_t n = c + r < c1 ? a.I - (i0 + col) : 0;
-        ra[i] = raw8((const T*)a.a + (c + r) * a.lda + i0 + col, n);
-      } else {
-        const int64_t n = i0 + r < a.I ? c1 - (c + col) : 0;
-        ra[i] = raw8((const T*)a.a + (i0 + r) * a.lda + c + col, n);
-      }
+  for (int i = 0; i < A::kPer; ++i) {
+    const int q = i * NT + tid, r = q / A::kRow, col = A::place(r, q % A::kRow) * 8;
+    ca[i] = TA ? r : col;
+    pa[i] = (const T*)a.a + (TA ? (c0 + r) * a.lda + i0 + col : min(i0 + r, a.I - 1) * a.lda + c0 + col);
+  }
+#pragma unroll
+  for (int i = 0; i < B::kPer; ++i) {
+    const int q = i * NT + tid, r = q / B::kRow, col = B::place(r, q % B::kRow) * 8;
+    cb[i] = TB ? r : col;
+    if constexpr (TB) {
+      pb[i] = (const T*)a.b + (c0 + r) * a.ldb + j0 + col;
+    } else {
+      const int64_t j = min(j0 + (GATED ? (r >> 6) * 32 + (r & 31) : r), a.J - 1);
+      pb[i] = (const T*)a.b + (j + (GATED && (r >> 5 & 1) ? a.J : 0)) * a.ldb + c0 + col;
     }
+  }
+  // every chunk of a whole step exists but for those across the operand's edge
+  const bool inner = (!TA || i0 + BI <= a.I) && (!TB || j0 + BJ <= a.J);
+  u32x4 ra[D][A::kPer], rb[D][B::kPer];
+  auto load = [&](u32x4 (&va)[A::kPer], u32x4 (&vb)[B::kPer], int s) {
+    const int64_t c = (int64_t)s * kC, left = c1 - c0 - c;
+    if (left >= kC && inner) {
 #pragma unroll
-    for (int i = 0; i < B::kPer; ++i) {
-      const int q = i * NT + tid, r = q / B::kRow, col = B::place(r, q % B::kRow) * 8;
-      if constexpr (TB) {
-        const int64_t n = c + r < c1 ? a.J - (j0 + col) : 0;
-        rb[i] = raw8((const T*)a.b + (c + r) * a.ldb + j0 + col, n);
-      } else {
-        int64_t row;
-        bool there;
-        b_row<GATED>(r, j0, a.J, row, there);
-        rb[i] = raw8((const T*)a.b + row * a.ldb + c + col, there ? c1 - (c + col) : 0);
+      for (int i = 0; i < A::kPer; ++i) va[i] = *(const u32x4_a2*)(pa[i] + (TA ? c * a.lda : c));
+#pragma unroll
+      for (int i = 0; i < B::kPer; ++i) vb[i] = *(const u32x4_a2*)(pb[i] + (TB ? c * a.ldb : c));
+    } else if (left > 0) {
+#pragma unroll
+      for (int i = 0; i < A::kPer; ++i) {
+        const int col = A::place((i * NT + tid) / A::kRow, (i * NT + tid) % A::kRow) * 8;
+        va[i] = raw8(pa[i] + (TA ? c * a.lda : c), TA ? (ca[i] < left ? a.I - (i0 + col) : 0) : left - ca[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < B::kPer; ++i) {
+        const int col = B::place((i * NT + tid) / B::kRow, (i * NT + tid) % B::kRow) * 8;
+        vb[i] = raw8(pb[i] + (TB ? c * a.ldb : c), TB ? (cb[i] < left ? a.J - (j0 + col) : 0) : left - cb[i]);
       }
     }
   };
-  auto stage = [&](int s) {
+  auto stage = [&](const u32x4 (&va)[A::kPer], const u32x4 (&vb)[B::kPer], int s) {
 #pragma unroll
-    for (int i = 0; i < A::kPer; ++i) *(u32x4*)(lds[s] + (i * NT + tid) * 8) = ra[i];
+    for (int i = 0; i < A::kPer; ++i) *(u32x4*)(lds[s & 1] + (i * NT + tid) * 8) = va[i];
 #pragma unroll
-    for (int i = 0; i < B::kPer; ++i) *(u32x4*)(lds[s] + BI * kC + (i * NT + tid) * 8) = rb[i];
+    for (int i = 0; i < B::kPer; ++i) *(u32x4*)(lds[s & 1] + BI * kC + (i * NT + tid) * 8) = vb[i];
   };
 
   f32x4 acc[TI][TJ];
@@ -129,30 +148,39 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+#pragma unroll
+  for (int u = 0; u < D; ++u) load(ra[u], rb[u], u);
   if (steps > 0) {
-    load(c0);
-    stage(0);
+    stage(ra[0], rb[0], 0);
+    load(ra[0], rb[0], D);
   }
   __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) load(c0 + (int64_t)(s + 1) * kC);
-    const lds_short *la = (lds_short*)lds[s & 1], *lb = la + BI * kC;
+  for (int s0 = 0; s0 < steps; s0 += D) {
 #pragma unroll
-    for (int kk = 0; kk < kC / 32; ++kk) {
-      s16x8 fa[TI], fb[TJ];
+    for (int d = 0; d < D; ++d) {
+      const int s = s0 + d;
+      if (s < steps) {
+        const lds_short *la = (lds_short*)lds[s & 1], *lb = la + BI * kC;
 #pragma unroll
-      for (int i = 0; i < TI; ++i) fa[i] = A::fragment(la, i, kk, lane, wi);
+        for (int kk = 0; kk < kC / 32; ++kk) {
+          s16x8 fa[TI], fb[TJ];
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) fb[j] = B::fragment(lb, j, kk, lane, wj);
+          for (int i = 0; i < TI; ++i) fa[i] = A::fragment(la, i, kk, lane, wi);
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
+          for (int j = 0; j < TJ; ++j) fb[j] = B::fragment(lb, j, kk, lane, wj);
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[j], fa[i], acc[i][j], T{});
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[j], fa[i], acc[i][j], T{});
+        }
+        if (s + 1 < steps) {
+          stage(ra[(d + 1) % D], rb[(d + 1) % D], s + 1);
+          load(ra[(d + 1) % D], rb[(d + 1) % D], s + 1 + D);
+        }
+        __syncthreads();
+      }
     }
-    if (s + 1 < steps) stage((s + 1) & 1);
-    __syncthreads();
   }
-
   write_tile<T, PAIRED, GATED, TI, TJ>(a, acc, i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
@@ -238,6 +266,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   }
   const T* pa = (const T*)a.a + (TA ? c0 * a.lda + i0 : i0 * a.lda + c0);
   const T* pb = (const T*)a.b + (TB ? c0 * a.ldb + j0 : j0 * a.ldb + c0);
+  const int64_t whole = (c1 - c0 + 7) & ~(int64_t)7;  // a last chunk's filling is its row's own
   constexpr int kPast = 0x7FFFFFF0;  // an offset past every range
   // past the last step the ranges are empty, so every step issues as many loads
   auto stage = [&](lds_short* la, int s) {
@@ -250,7 +279,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
 #pragma unroll
       for (int i = 0; i < A::kPer; ++i) dma16(r, la + (i * NT + wave * 64) * 8, oa[i]);
     } else {
-      const auto r = range_of(pa, ((rows_a - 1) * a.lda + (c1 - c0)) * 2);
+      const auto r = range_of(pa, ((rows_a - 1) * a.lda + whole) * 2);
 #pragma unroll
       for (int i = 0; i < A::kPer; ++i) {
         const int o = oa[i] + s * kC * 2;
@@ -264,7 +293,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
 #pragma unroll
       for (int i = 0; i < B::kPer; ++i) dma16(r, lb + (i * NT + wave * 64) * 8, ob[i]);
     } else {
-      const int64_t bytes = ((rows_b - 1) * a.ldb + (c1 - c0)) * 2;
+      const int64_t bytes = ((rows_b - 1) * a.ldb + whole) * 2;
       const auto r = range_of(pb, bytes);
       const auto up = range_of(GATED ? pb + a.J * a.ldb : pb, bytes);
 #pragma unroll
@@ -315,14 +344,15 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   write_tile<T, PAIRED, GATED, TI, TJ>(a, acc, i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
-// whether every 16-byte chunk of both operands is aligned and, along c, whole
+// whether every 16-byte chunk of both operands is aligned and, along c, whole or
+// filled up with zeros
 template <bool TA, bool TB>
 bool chunked(const TileArgs& a) {
   return aligned(a.a, 16) && aligned(a.b, 16) && a.lda % 8 == 0 && a.ldb % 8 == 0 &&
-         ((TA && TB) || a.C % 8 == 0);
+         ((TA && TB) || a.C % 8 == 0 || a.padded);
 }
 
-// S: stages fed by direct loads, or 0 for the kernel that stages through registers
+// S: stages fed by direct loads, or, negative, steps loaded ahead through registers
 template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S>
 int launch_tile(TileArgs a, hipStream_t s) {
   const int64_t out = GATED ? BJ / 2 : BJ;
@@ -334,7 +364,7 @@ int launch_tile(TileArgs a, hipStream_t s) {
   a.tiles_j = (uint32_t)tj;
   const dim3 grid(a.tiles_i * a.tiles_j * a.splits);
   if constexpr (S > 0) return launch(k_tile_dma<T, TA, TB, BI, BJ, WI, WJ, GATED, S>, grid, dim3(NT), s, a);
-  else return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED>, grid, dim3(NT), s, a);
+  else return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED, -S>, grid, dim3(NT), s, a);
 }
 
 }  // namespace
