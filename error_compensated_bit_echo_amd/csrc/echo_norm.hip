@@ -36,45 +36,46 @@ struct NormArgs {
   float scale, eps;
 };
 
-// threads of a workgroup whose rows take W wavefronts
-constexpr int threads_of(int W) { return W < 4 ? 256 : 64 * W; }
+// WAVES = 1: a row to a wavefront, four rows side by side in a workgroup.
+// WAVES > 1: a row to the workgroup, which has up to so many wavefronts (fewer
+// leave the compiler more registers).
+constexpr int kSideBySide = 4;
+constexpr int kMostWaves = 16;
+constexpr int threads_of(int WAVES) { return 64 * (WAVES > 1 ? WAVES : kSideBySide); }
 
-// Sums over the W wavefronts of a row, double-buffered by the row's parity: a
-// slot is written again two rows later, and the barrier of the row between
-// keeps a late reader apart from it.
-template <int W, int SLOTS>
+// Sums over the wavefronts of a row, double-buffered by the row's parity: a slot
+// is written again two rows later, and the barrier of the row between keeps a
+// late reader apart from it.
+template <bool MANY>
 struct RowSums {
-  float* lds;  // [2][SLOTS][W]
-  uint32_t wave, parity;
+  float* lds;  // [2][4][kMostWaves]
+  uint32_t wave, waves, parity;
+  __device__ __forceinline__ float add(const float* p) const {
+    float s = p[0];
+    for (uint32_t i = 1; i < waves; ++i) s += p[i];
+    return s;
+  }
   __device__ __forceinline__ float sum(float v, int slot) {
     v = wave_sum(v);
-    if constexpr (W == 1) return v;
-    float* p = lds + (parity * SLOTS + slot) * W;
+    if constexpr (!MANY) return v;
+    float* p = lds + (parity * 4 + slot) * kMostWaves;
     if ((threadIdx.x & 63) == 0) p[wave] = v;
     __syncthreads();
-    float s = p[0];
-#pragma unroll
-    for (int i = 1; i < W; ++i) s += p[i];
-    return s;
+    return add(p);
   }
   // two sums behind one barrier
   __device__ __forceinline__ void sum2(float& a, float& b, int slot) {
     a = wave_sum(a);
     b = wave_sum(b);
-    if constexpr (W > 1) {
-      float* p = lds + (parity * SLOTS + slot) * W;
+    if constexpr (MANY) {
+      float* p = lds + (parity * 4 + slot) * kMostWaves;
       if ((threadIdx.x & 63) == 0) {
         p[wave] = a;
-        p[W + wave] = b;
+        p[kMostWaves + wave] = b;
       }
       __syncthreads();
-      a = p[0];
-      b = p[W];
-#pragma unroll
-      for (int i = 1; i < W; ++i) {
-        a += p[i];
-        b += p[W + i];
-      }
+      a = add(p);
+      b = add(p + kMostWaves);
     }
   }
 };
@@ -82,8 +83,8 @@ struct RowSums {
 // Mean and reciprocal deviation of the row in v.  The layer norm's variance is
 // the mean square about the mean, from registers, so a mean far from zero
 // costs no digits.
-template <int ITEMS, typename Sums>
-__device__ __forceinline__ void moments(const float (&v)[ITEMS][8], const int (&n)[ITEMS], int kind,
+template <RowEnd END, int ITEMS, typename Sums>
+__device__ __forceinline__ void moments(const float (&v)[ITEMS][8], const Place<END> (&at)[ITEMS], int kind,
                                         float eps, float inv_h, Sums& sums, int slot, float& mean,
                                         float& rstd) {
   mean = 0.f;
@@ -92,7 +93,7 @@ __device__ __forceinline__ void moments(const float (&v)[ITEMS][8], const int (&
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += e < n[i] ? v[i][e] : 0.f;
+      for (int e = 0; e < 8; ++e) s += at[i].only(e, v[i][e]);
     mean = sums.sum(s, slot) * inv_h;
   }
   float q = 0.f;
@@ -100,77 +101,121 @@ __device__ __forceinline__ void moments(const float (&v)[ITEMS][8], const int (&
   for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float c = e < n[i] ? v[i][e] - mean : 0.f;
+      const float c = at[i].only(e, v[i][e] - mean);
       q = fmaf(c, c, q);
     }
   rstd = 1.0f / sqrtf(sums.sum(q, slot + 1) * inv_h + eps);
 }
 
-// v <- (v - mean) rstd w + b on the thread's columns
+// The thread's columns of a vector along the row (a weight, a bias, a gate row),
+// fetched before they are needed; absent ones are `none`.
 template <typename T, int ITEMS>
-__device__ __forceinline__ void apply_norm(float (&v)[ITEMS][8], const int (&n)[ITEMS],
-                                           const int (&col)[ITEMS], float mean, float rstd,
-                                           const T* w, const T* b) {
+struct RowVector {
+  Raw<T> raw[ITEMS];
+  const T* row;
+  template <typename P>
+  __device__ __forceinline__ void fetch(const void* p, const P (&at)[ITEMS], int H) {
+    row = (const T*)p;
+    if (!row) return;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) raw[i] = at[i].template fetch<false>(row, H);
+  }
+  // keeps the words packed across a loop: unpacked ahead of it they would take
+  // twice the registers
+  __device__ __forceinline__ void keep_packed() {
+    if (!row) return;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) keep(raw[i]);
+  }
+};
+
+// A thread's vectors of a row, `across` threads to a row.
+template <RowEnd END, int ITEMS>
+struct Places;
+template <RowEnd END>
+struct Places<END, 1> {
+  Place<END> at[1];
+  int col[1];
+  __device__ __forceinline__ Places(int thread, int, int H) : at{{thread * 8, H}}, col{thread * 8} {}
+};
+template <RowEnd END>
+struct Places<END, 2> {
+  Place<END> at[2];
+  int col[2];
+  __device__ __forceinline__ Places(int thread, int across, int H)
+      : at{{thread * 8, H}, {(thread + across) * 8, H}}, col{thread * 8, (thread + across) * 8} {}
+};
+
+// v <- (v - mean) rstd w + b on the thread's columns
+template <RowEnd END, typename T, int ITEMS>
+__device__ __forceinline__ void apply_norm(float (&v)[ITEMS][8], const Place<END> (&at)[ITEMS], float mean,
+                                           float rstd, const RowVector<T, ITEMS>& w,
+                                           const RowVector<T, ITEMS>& b) {
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    if (n[i] <= 0) continue;
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] = (v[i][e] - mean) * rstd;
-    if (w) {
-      load_n<false>(w + col[i], n[i], f);
+    if (w.row) {
+      at[i].unpack(w.raw[i], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] *= f[e];
     }
-    if (b) {
-      load_n<false>(b + col[i], n[i], f);
+    if (b.row) {
+      at[i].unpack(b.raw[i], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] += f[e];
     }
   }
 }
 
-template <typename T, typename S, int W, int ITEMS>
-__global__ __launch_bounds__(threads_of(W)) void k_norm(NormArgs a) {
-  constexpr int kRows = W < 4 ? 4 / W : 1;  // rows a workgroup works on at a time
-  __shared__ float slots[W > 1 ? 2 * 4 * W : 1];
+template <typename T, typename S, int WAVES, int ITEMS, RowEnd END>
+__global__ __launch_bounds__(threads_of(WAVES)) void k_norm(NormArgs a) {
+  constexpr bool MANY = WAVES > 1;
+  constexpr int kRows = MANY ? 1 : kSideBySide;  // rows a workgroup works on at a time
+  __shared__ float slots[MANY ? 2 * 4 * kMostWaves : 1];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  RowSums<W, 4> sums{slots, wave % W, 0};
+  const int across = MANY ? (int)blockDim.x : 64;  // threads of a row
+  RowSums<MANY> sums{slots, wave, blockDim.x >> 6, 0};
   const int H = (int)a.hidden;
   const float inv_h = 1.0f / (float)H;
-  int col[ITEMS], n[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    col[i] = ((int)(threadIdx.x % (64 * W)) + i * 64 * W) * 8;
-    n[i] = H - col[i];
-  }
-  for (int64_t row = (int64_t)blockIdx.x * kRows + wave / W; row < a.tokens;
+  const Places<END, ITEMS> places(MANY ? (int)threadIdx.x : (int)(threadIdx.x & 63), across, H);
+  const auto& at = places.at;
+  const auto& col = places.col;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + (MANY ? 0 : wave); row < a.tokens;
        row += (int64_t)gridDim.x * kRows, sums.parity ^= 1) {
     float v[ITEMS][8], h[ITEMS][8];
     const S* hp = (const S*)a.h + row * a.ld_h;
     const T* yp = (const T*)a.y + row * a.ld_y;
+    Raw<S> hr[ITEMS];
+    Raw<T> yr[ITEMS];
+    RowVector<T, ITEMS> gate, w_post, b_post, w_pre, b_pre;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = v[i][e] = 0.f;
-      if (n[i] > 0) {
-        load_n<true>(hp + col[i], n[i], h[i]);
-        if (a.y) load_n<true>(yp + col[i], n[i], v[i]);
-      }
+      hr[i] = at[i].template fetch<true>(hp, H);
+      if (a.y) yr[i] = at[i].template fetch<true>(yp, H);
     }
+    w_post.fetch(a.w_post, at, H);
+    b_post.fetch(a.b_post, at, H);
+    gate.fetch(a.rows_per_gate ? (const T*)a.gate + (int64_t)((uint32_t)row / a.rows_per_gate) * H : nullptr,
+                    at, H);
+    w_pre.fetch(a.w_pre, at, H);
+    b_pre.fetch(a.b_pre, at, H);
     float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) at[i].unpack(hr[i], h[i]);
     if (a.y) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) at[i].unpack(yr[i], v[i]);
       if (a.post != ECHO_NORM_NONE) {
-        moments<ITEMS>(v, n, a.post, a.eps, inv_h, sums, 0, mean1, rstd1);
-        apply_norm<T, ITEMS>(v, n, col, mean1, rstd1, (const T*)a.w_post, (const T*)a.b_post);
+        moments(v, at, a.post, a.eps, inv_h, sums, 0, mean1, rstd1);
+        apply_norm<END, T, ITEMS>(v, at, mean1, rstd1, w_post, b_post);
       }
-      if (a.rows_per_gate) {
-        const T* g = (const T*)a.gate + (int64_t)((uint32_t)row / a.rows_per_gate) * H;
+      if (gate.row) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-          if (n[i] <= 0) continue;
           float f[8];
-          load_n<false>(g + col[i], n[i], f);
+          at[i].unpack(gate.raw[i], f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[i][e] *= f[e];
         }
@@ -183,18 +228,18 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm(NormArgs a) {
         S* op = (S*)a.h_out + row * a.ld_h;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i)
-          if (n[i] > 0) store_n<true>(op + col[i], n[i], h[i]);
+          at[i].template store<true>(op + col[i], h[i]);
       }
     }
     if (a.pre != ECHO_NORM_NONE) {
-      moments<ITEMS>(h, n, a.pre, a.eps, inv_h, sums, 2, mean2, rstd2);
-      apply_norm<T, ITEMS>(h, n, col, mean2, rstd2, (const T*)a.w_pre, (const T*)a.b_pre);
+      moments(h, at, a.pre, a.eps, inv_h, sums, 2, mean2, rstd2);
+      apply_norm<END, T, ITEMS>(h, at, mean2, rstd2, w_pre, b_pre);
       T* zp = (T*)a.z + row * H;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
-        if (n[i] > 0) store_n<true>(zp + col[i], n[i], h[i]);
+        at[i].template store<true>(zp + col[i], h[i]);
     }
-    if (a.stats && threadIdx.x % (64 * W) == 0) {
+    if (a.stats && (MANY ? threadIdx.x : threadIdx.x & 63) == 0) {
       a.stats[row] = mean1;
       a.stats[a.tokens + row] = rstd1;
       a.stats[2 * a.tokens + row] = mean2;
@@ -240,27 +285,27 @@ __device__ __forceinline__ void zero(float (&v)[ITEMS][8]) {
 
 // The accumulators of a workgroup, its rows' wavefronts added in order, to
 // out[hidden] (binary32 partial sums or, for a whole gate row, its gradient).
-template <typename O, int W, int ITEMS>
-__device__ __forceinline__ void flush(float (&acc)[ITEMS][8], const int (&n)[ITEMS],
-                                      const int (&col)[ITEMS], O* out, int H, float* comb) {
-  if constexpr (W >= 4) {
+template <typename O, bool MANY, int ITEMS>
+__device__ __forceinline__ void flush(float (&acc)[ITEMS][8], const int (&col)[ITEMS], O* out, int H,
+                                      float* comb) {
+  if constexpr (MANY) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
-      if (n[i] > 0) store_n<false>(out + col[i], n[i], acc[i]);
+      if (col[i] < H) store_n<false>(out + col[i], H - col[i], acc[i]);
   } else {
     __syncthreads();
     const uint32_t w = threadIdx.x >> 6;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
-      if (n[i] > 0) {
+      if (col[i] < H) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) comb[w * (512 * ITEMS) + col[i] + e] = acc[i][e];
       }
     __syncthreads();
-    for (int c = threadIdx.x; c < H; c += 256) {
+    for (int c = threadIdx.x; c < H; c += 64 * kSideBySide) {
       float s = comb[c];
 #pragma unroll
-      for (int k = 1; k < 4; ++k) s += comb[k * (512 * ITEMS) + c];
+      for (int k = 1; k < kSideBySide; ++k) s += comb[k * (512 * ITEMS) + c];
       out[c] = from_f32<O>(s);
     }
   }
@@ -270,22 +315,27 @@ __device__ __forceinline__ void flush(float (&acc)[ITEMS][8], const int (&n)[ITE
 // norm's parameters have gradients (fewer accumulators, so more rows in
 // flight).  A workgroup walks `chunk` consecutive rows and keeps the sums over
 // them in registers, so the row data is read once for all outputs.
-template <typename T, typename S, int W, int ITEMS, bool FULL>
-__global__ __launch_bounds__(threads_of(W)) void k_norm_backward(NormBackArgs a) {
-  static_assert(W == 1 || W >= 4, "rows of a workgroup");
-  constexpr int kRows = W < 4 ? 4 / W : 1;
-  __shared__ float slots[W > 1 ? 2 * 4 * W : 1];
-  __shared__ float comb[W < 4 ? 4 * 512 * ITEMS : 1];
+template <typename T, typename S, int WAVES, int ITEMS, bool FULL, RowEnd END>
+__global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1 ? 3 : 1) void k_norm_backward(
+    NormBackArgs a) {
+  constexpr bool MANY = WAVES > 1;
+  constexpr int kRows = MANY ? 1 : kSideBySide;
+  __shared__ float slots[MANY ? 2 * 4 * kMostWaves : 1];
+  __shared__ float comb[MANY ? 1 : kSideBySide * 512 * ITEMS];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  RowSums<W, 4> sums{slots, wave % W, 0};
+  const int across = MANY ? (int)blockDim.x : 64;
+  RowSums<MANY> sums{slots, wave, blockDim.x >> 6, 0};
   const int H = (int)a.hidden;
   const float inv_h = 1.0f / (float)H;
-  int col[ITEMS], n[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    col[i] = ((int)(threadIdx.x % (64 * W)) + i * 64 * W) * 8;
-    n[i] = H - col[i];
-  }
+  const Places<END, ITEMS> places(MANY ? (int)threadIdx.x : (int)(threadIdx.x & 63), across, H);
+  const auto& at = places.at;
+  const auto& col = places.col;
+  // the thread's columns of the weights stay in registers for all its rows
+  RowVector<T, ITEMS> w_pre, w_post, b_post, gate;
+  w_pre.fetch(a.w_pre, at, H);
+  w_post.fetch(FULL ? a.w_post : nullptr, at, H);
+  b_post.fetch(FULL ? a.b_post : nullptr, at, H);
+  gate.row = nullptr;
   int64_t r0, r1;
   if (a.gate_sum == kGatePart) {
     const int64_t g = blockIdx.x / a.blocks_per_gate, s = blockIdx.x % a.blocks_per_gate;
@@ -305,44 +355,50 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(NormBackArgs a)
   int64_t s1;
   for (int64_t s0 = r0; s0 < r1; s0 = s1) {
     s1 = FULL && a.gate_sum == kGateWhole ? min(s0 + (int64_t)a.rows_per_gate, r1) : r1;
-    for (int64_t row = s0 + wave / W; row < s1; row += kRows, sums.parity ^= 1) {
+    for (int64_t row = s0 + (MANY ? 0 : wave); row < s1; row += kRows, sums.parity ^= 1) {
       float d[ITEMS][8];   // dh' + N_pre'(dz), then dh
       float hat[ITEMS][8], g[ITEMS][8];
-      zero(d);
-      zero(hat);
-      zero(g);
       const T* dzp = (const T*)a.dz + row * H;
       const S* dhp = (const S*)a.dh_out + row * H;
       const S* hp = (const S*)a.h_out + row * a.ld_h;
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-        if (n[i] > 0) {
-          if (a.dh_out) load_n<true>(dhp + col[i], n[i], d[i]);
-          if (a.pre != ECHO_NORM_NONE) {
-            load_n<true>(hp + col[i], n[i], hat[i]);
-            load_n<true>(dzp + col[i], n[i], g[i]);
-          }
-        }
-      float y[FULL ? ITEMS : 1][8];
-      zero(y);
-      if constexpr (FULL) {
-        const T* yp = (const T*)a.y + row * a.ld_y;
-        if (a.y)
-#pragma unroll
-          for (int i = 0; i < ITEMS; ++i)
-            if (n[i] > 0) load_n<true>(yp + col[i], n[i], y[i]);
-      }
+      const T* yp = (const T*)a.y + row * a.ld_y;
+      w_pre.keep_packed();
+      w_post.keep_packed();
+      b_post.keep_packed();
+      Raw<S> dr[ITEMS], hr[ITEMS];
+      Raw<T> zr[ITEMS], yr[ITEMS];
+      float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
       if (a.pre != ECHO_NORM_NONE) {
-        const float mean = a.stats[2 * a.tokens + row], rstd = a.stats[3 * a.tokens + row];
+        mean2 = a.stats[2 * a.tokens + row];
+        rstd2 = a.stats[3 * a.tokens + row];
+      }
+      if (FULL && a.post != ECHO_NORM_NONE) {
+        mean1 = a.stats[row];
+        rstd1 = a.stats[a.tokens + row];
+      }
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        if (a.pre != ECHO_NORM_NONE) {
+          hr[i] = at[i].template fetch<true>(hp, H);
+          zr[i] = at[i].template fetch<true>(dzp, H);
+        }
+        if (a.dh_out) dr[i] = at[i].template fetch<true>(dhp, H);
+        if (FULL && a.y) yr[i] = at[i].template fetch<true>(yp, H);
+      }
+      if (FULL && a.rows_per_gate)
+        gate.fetch((const T*)a.gate + (int64_t)((uint32_t)row / a.rows_per_gate) * H, at, H);
+      zero(d);
+      if (a.pre != ECHO_NORM_NONE) {
         float sh = 0.f, sg = 0.f;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-          if (n[i] <= 0) continue;
           float w[8];
-          if (a.w_pre) load_n<false>((const T*)a.w_pre + col[i], n[i], w);
+          at[i].unpack(hr[i], hat[i]);
+          at[i].unpack(zr[i], g[i]);
+          if (a.w_pre) at[i].unpack(w_pre.raw[i], w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            hat[i][e] = e < n[i] ? (hat[i][e] - mean) * rstd : 0.f;
+            hat[i][e] = at[i].only(e, (hat[i][e] - mean2) * rstd2);
             dw2[i][e] = fmaf(g[i][e], hat[i][e], dw2[i][e]);
             db2[i][e] += g[i][e];
             if (a.w_pre) g[i][e] *= w[e];
@@ -361,13 +417,21 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(NormBackArgs a)
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            d[i][e] = e < n[i] ? fmaf(rstd, (g[i][e] - sg) - hat[i][e] * sh, d[i][e]) : 0.f;
+          for (int e = 0; e < 8; ++e) d[i][e] = at[i].only(e, rstd2 * ((g[i][e] - sg) - hat[i][e] * sh));
+      }
+      if (a.dh_out) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          float f[8];
+          at[i].unpack(dr[i], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[i][e] += f[e];
+        }
       }
       S* op = (S*)a.dh + row * H;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
-        if (n[i] > 0) store_n<true>(op + col[i], n[i], d[i]);
+        at[i].template store<true>(op + col[i], d[i]);
       // du = scale gate dh; the gate's and the post norm's gradients from it
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
@@ -375,18 +439,16 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(NormBackArgs a)
         for (int e = 0; e < 8; ++e) d[i][e] *= a.scale;
       T* dyp = (T*)a.dy + row * H;
       if constexpr (FULL) {
-        const float mean = a.stats ? a.stats[row] : 0.f, rstd = a.stats ? a.stats[a.tokens + row] : 1.f;
-        const uint32_t gr = a.rows_per_gate ? (uint32_t)row / a.rows_per_gate : 0;
-        const T* gp = (const T*)a.gate + (int64_t)gr * H;
+        float y[ITEMS][8];
         float sh = 0.f, sg = 0.f;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-          if (n[i] <= 0) continue;
           float w[8], b[8];
-          if (a.w_post) load_n<false>((const T*)a.w_post + col[i], n[i], w);
+          if (a.y) at[i].unpack(yr[i], y[i]);
+          if (a.w_post) at[i].unpack(w_post.raw[i], w);
           if (a.post != ECHO_NORM_NONE) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][e] = e < n[i] ? (y[i][e] - mean) * rstd : 0.f;
+            for (int e = 0; e < 8; ++e) y[i][e] = at[i].only(e, (y[i][e] - mean1) * rstd1);
           }
           if (a.rows_per_gate) {
             if (a.gate_sum != kGateNone) {
@@ -394,20 +456,20 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(NormBackArgs a)
 #pragma unroll
               for (int e = 0; e < 8; ++e) u[e] = a.w_post ? y[i][e] * w[e] : y[i][e];
               if (a.b_post) {
-                load_n<false>((const T*)a.b_post + col[i], n[i], b);
+                at[i].unpack(b_post.raw[i], b);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) u[e] += b[e];
               }
               if (a.gate_sum == kGateRow) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) u[e] *= d[i][e];
-                store_n<true>((T*)a.dgate + row * H + col[i], n[i], u);
+                at[i].template store<true>((T*)a.dgate + row * H + col[i], u);
               } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dg[i][e] = fmaf(u[e], d[i][e], dg[i][e]);
               }
             }
-            load_n<false>(gp + col[i], n[i], b);
+            at[i].unpack(gate.raw[i], b);
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[i][e] *= b[e];
           }
@@ -434,29 +496,29 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(NormBackArgs a)
 #pragma unroll
           for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[i][e] = rstd * ((d[i][e] - sg) - y[i][e] * sh);
+            for (int e = 0; e < 8; ++e) d[i][e] = rstd1 * ((d[i][e] - sg) - y[i][e] * sh);
         }
       }
       if (a.dy)
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i)
-          if (n[i] > 0) store_n<true>(dyp + col[i], n[i], d[i]);
+          at[i].template store<true>(dyp + col[i], d[i]);
     }
     if constexpr (FULL) {
       if (a.gate_sum == kGateWhole) {
-        flush<T, W, ITEMS>(dg, n, col, (T*)a.dgate + s0 / a.rows_per_gate * H, H, comb);
+        flush<T, MANY, ITEMS>(dg, col, (T*)a.dgate + s0 / a.rows_per_gate * H, H, comb);
         zero(dg);
       }
     }
   }
   const int64_t plane = (int64_t)gridDim.x * H;
   float* p = a.part + (int64_t)blockIdx.x * H;
-  if (a.want >> kDwPre & 1) flush<float, W, ITEMS>(dw2, n, col, p + kDwPre * plane, H, comb);
-  if (a.want >> kDbPre & 1) flush<float, W, ITEMS>(db2, n, col, p + kDbPre * plane, H, comb);
+  if (a.want >> kDwPre & 1) flush<float, MANY, ITEMS>(dw2, col, p + kDwPre * plane, H, comb);
+  if (a.want >> kDbPre & 1) flush<float, MANY, ITEMS>(db2, col, p + kDbPre * plane, H, comb);
   if constexpr (FULL) {
-    if (a.want >> kDwPost & 1) flush<float, W, ITEMS>(dw1, n, col, p + kDwPost * plane, H, comb);
-    if (a.want >> kDbPost & 1) flush<float, W, ITEMS>(db1, n, col, p + kDbPost * plane, H, comb);
-    if (a.want >> kDgate & 1) flush<float, W, ITEMS>(dg, n, col, p + kDgate * plane, H, comb);
+    if (a.want >> kDwPost & 1) flush<float, MANY, ITEMS>(dw1, col, p + kDwPost * plane, H, comb);
+    if (a.want >> kDbPost & 1) flush<float, MANY, ITEMS>(db1, col, p + kDbPost * plane, H, comb);
+    if (a.want >> kDgate & 1) flush<float, MANY, ITEMS>(dg, col, p + kDgate * plane, H, comb);
   }
 }
 
@@ -478,8 +540,17 @@ __global__ __launch_bounds__(1024) void k_norm_part_sum(PartSumArgs a) {
     const uint32_t nb = a.per_row[p];
     const float* src = a.part[p] + (int64_t)r * nb * a.hidden;
     float s = 0.f;
-    if (col < a.hidden)
-      for (uint32_t b = k; b < nb; b += 32) s += src[(int64_t)b * a.hidden + col];
+    if (col < a.hidden) {
+      uint32_t b = k;
+      for (; b + 7 * 32 < nb; b += 8 * 32) {  // eight loads on their way at once
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = src[(int64_t)(b + e * 32) * a.hidden + col];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[e];
+      }
+      for (; b < nb; b += 32) s += src[(int64_t)b * a.hidden + col];
+    }
     __syncthreads();
     lds[k][c] = s;
     __syncthreads();
@@ -539,16 +610,23 @@ int check_desc(const echo_norm_desc* d, Geometry& g) {
   return ECHO_SUCCESS;
 }
 
-// Wavefronts and vectors per row: the fewest that hold it, so that a
-// wavefront's 64 lanes have work.  Rows to 1024 elements take one wavefront
-// and need no barrier.
-struct RowShape { int waves, items; };
-constexpr RowShape kShapes[] = {{1, 1}, {1, 2}, {4, 1}, {4, 2}, {16, 1}, {16, 2}};
+// Wavefronts of a row and vectors of a thread.  Short rows take one wavefront and
+// need no barrier; longer ones as many as hold them.  The forward pass holds two
+// vectors a thread past 2048 elements (8192 x 4096: 48.5 us against 51.7 with one,
+// which has twice the wavefronts to wait for at a barrier); the backward pass,
+// whose accumulators fill the registers, one.
+struct RowShape {
+  int waves, items, threads;  // waves: the kernel's WAVES
+  int64_t rows;               // of a workgroup at a time
+};
+enum Pass { kForward, kBackPlain, kBackFull };
 
-int shape_of(int64_t hidden) {
-  int i = 0;
-  while (kShapes[i].waves * kShapes[i].items * 512 < hidden) ++i;
-  return i;
+RowShape shape_of(int64_t hidden, Pass pass) {
+  if (hidden <= 512) return {1, 1, 64 * kSideBySide, kSideBySide};
+  if (hidden <= 1024 && pass != kBackFull) return {1, 2, 64 * kSideBySide, kSideBySide};
+  const int items = hidden <= (pass == kForward ? 2048 : 512 * kMostWaves) ? 1 : 2;
+  const int waves = (int)((hidden + 512 * items - 1) / (512 * items));
+  return {waves <= 8 ? 8 : kMostWaves, items, waves * 64, 1};
 }
 
 // Rows of a workgroup of the backward pass, and how many workgroups that is.
@@ -558,9 +636,12 @@ struct Walk {
   int32_t gate_sum;
 };
 
-Walk walk_of(int64_t T, int64_t H, int64_t gate_rows, bool want_gate) {
-  const int64_t rows = kShapes[shape_of(H)].waves == 1 ? 4 : 1;  // side by side
-  const int64_t most = 1024;                                       // workgroups
+Walk walk_of(int64_t T, int64_t H, int64_t gate_rows, bool want_gate, Pass pass) {
+  const RowShape shape = shape_of(H, pass);
+  const int64_t rows = shape.rows;
+  // as many workgroups as are in residence, by the kernels' registers
+  const int resident = pass == kBackFull ? 12 : 16;  // wavefronts of a compute unit
+  const int64_t most = 256 * (resident * 64 >= shape.threads ? resident * 64 / shape.threads : 1);
   Walk w = {};
   int64_t chunk = (T + most - 1) / most;
   chunk = (chunk + rows - 1) / rows * rows;
@@ -586,37 +667,55 @@ Walk walk_of(int64_t T, int64_t H, int64_t gate_rows, bool want_gate) {
   return w;
 }
 
+template <typename T, typename S, RowEnd END>
+int launch_norm(const NormArgs& a, hipStream_t s) {
+  const RowShape r = shape_of(a.hidden, kForward);
+  const int64_t want = (a.tokens + r.rows - 1) / r.rows;
+  const int64_t cap = 0xFFFFFFFFu / (uint32_t)r.threads;
+  const dim3 grid((uint32_t)(want < cap ? want : cap)), block(r.threads);
+  if constexpr (END == kShort) return launch(k_norm<T, S, 1, 1, END>, grid, block, s, a);
+  else switch (r.waves * 4 + r.items) {
+    case 4 + 1: return launch(k_norm<T, S, 1, 1, END>, grid, block, s, a);
+    case 4 + 2: return launch(k_norm<T, S, 1, 2, END>, grid, block, s, a);
+    case 32 + 1: return launch(k_norm<T, S, 8, 1, END>, grid, block, s, a);
+    case 32 + 2: return launch(k_norm<T, S, 8, 2, END>, grid, block, s, a);
+    default: return launch(k_norm<T, S, 16, 2, END>, grid, block, s, a);
+  }
+}
+
 template <typename T, typename S>
 int launch_norm(const NormArgs& a, hipStream_t s) {
-  const int i = shape_of(a.hidden);
-  const int W = kShapes[i].waves;
-  const int64_t rows = W < 4 ? 4 / W : 1;
-  const int64_t want = (a.tokens + rows - 1) / rows;
-  const uint32_t cap = 0xFFFFFFFFu / (uint32_t)threads_of(W);
-  const dim3 grid((uint32_t)(want < cap ? want : cap)), block(threads_of(W));
-  switch (i) {
-#define ECHO_CASE(k) \
-  case k: return launch(k_norm<T, S, kShapes[k].waves, kShapes[k].items>, grid, block, s, a);
-    ECHO_CASE(0) ECHO_CASE(1) ECHO_CASE(2) ECHO_CASE(3) ECHO_CASE(4) ECHO_CASE(5)
-#undef ECHO_CASE
+  if (a.hidden < 8) return launch_norm<T, S, kShort>(a, s);
+  return a.hidden % 8 ? launch_norm<T, S, kTail>(a, s) : launch_norm<T, S, kWhole>(a, s);
+}
+
+template <typename T, typename S, bool FULL, RowEnd END>
+int launch_norm_backward(const NormBackArgs& a, uint32_t blocks, hipStream_t s) {
+  const RowShape r = shape_of(a.hidden, FULL ? kBackFull : kBackPlain);
+  const dim3 grid(blocks), block(r.threads);
+  if constexpr (END == kShort) return launch(k_norm_backward<T, S, 1, 1, FULL, END>, grid, block, s, a);
+  else switch (r.waves * 4 + r.items) {
+    case 4 + 1: return launch(k_norm_backward<T, S, 1, 1, FULL, END>, grid, block, s, a);
+    case 4 + 2:
+      if constexpr (!FULL) return launch(k_norm_backward<T, S, 1, 2, FULL, END>, grid, block, s, a);
+      return ECHO_ERR_SHAPE;
+    case 32 + 1: return launch(k_norm_backward<T, S, 8, 1, FULL, END>, grid, block, s, a);
+    case 64 + 1: return launch(k_norm_backward<T, S, 16, 1, FULL, END>, grid, block, s, a);
+    default: return launch(k_norm_backward<T, S, 16, 2, FULL, END>, grid, block, s, a);
   }
-  return ECHO_ERR_SHAPE;
+}
+
+template <typename T, typename S, RowEnd END>
+int launch_norm_backward(const NormBackArgs& a, uint32_t blocks, bool full, hipStream_t s) {
+  return full ? launch_norm_backward<T, S, true, END>(a, blocks, s)
+              : launch_norm_backward<T, S, false, END>(a, blocks, s);
 }
 
 template <typename T, typename S>
 int launch_norm_backward(const NormBackArgs& a, uint32_t blocks, bool full, hipStream_t s) {
-  const int i = shape_of(a.hidden);
-  const dim3 grid(blocks), block(threads_of(kShapes[i].waves));
-  switch (i) {
-#define ECHO_CASE(k)                                                                             \
-  case k:                                                                                        \
-    if (full)                                                                                    \
-      return launch(k_norm_backward<T, S, kShapes[k].waves, kShapes[k].items, true>, grid, block, s, a); \
-    return launch(k_norm_backward<T, S, kShapes[k].waves, kShapes[k].items, false>, grid, block, s, a);
-    ECHO_CASE(0) ECHO_CASE(1) ECHO_CASE(2) ECHO_CASE(3) ECHO_CASE(4) ECHO_CASE(5)
-#undef ECHO_CASE
-  }
-  return ECHO_ERR_SHAPE;
+  if (a.hidden < 8) return launch_norm_backward<T, S, kShort>(a, blocks, full, s);
+  return a.hidden % 8 ? launch_norm_backward<T, S, kTail>(a, blocks, full, s)
+                      : launch_norm_backward<T, S, kWhole>(a, blocks, full, s);
 }
 
 int run_norm(const NormArgs& a, int32_t t, int32_t st, hipStream_t s) {
@@ -700,9 +799,14 @@ int64_t echo_norm_backward_workspace(const echo_norm_desc* d) {
   const int rc = check_shape(d);
   if (rc) return rc;
   if (d->tokens == 0) return 0;
-  const Walk w = walk_of(d->tokens, d->hidden, d->gate_rows, true);
-  const Walk v = walk_of(d->tokens, d->hidden, d->gate_rows, false);
-  return (int64_t)kParts * (w.blocks > v.blocks ? w.blocks : v.blocks) * d->hidden * 4;
+  // whatever norms, and whether the gate's gradient is wanted or not
+  uint32_t most = 0;
+  for (const Pass pass : {kBackPlain, kBackFull})
+    for (const bool want_gate : {false, true}) {
+      const uint32_t blocks = walk_of(d->tokens, d->hidden, d->gate_rows, want_gate, pass).blocks;
+      if (blocks > most) most = blocks;
+    }
+  return (int64_t)kParts * most * d->hidden * 4;
 }
 
 int echo_norm_backward(const echo_norm_desc* d, const void* dz, const void* dh_out,
@@ -754,7 +858,8 @@ int echo_norm_backward(const echo_norm_desc* d, const void* dz, const void* dh_o
   al.allow_identical(dh, dh_out);
   if (!al.ok()) return ECHO_ERR_ALIAS;
 
-  const Walk w = walk_of(g.T, g.H, d->gate_rows, dgate != nullptr);
+  const bool full = post || d->gate_rows > 0;
+  const Walk w = walk_of(g.T, g.H, d->gate_rows, dgate != nullptr, full ? kBackFull : kBackPlain);
   PartSumArgs ps = {};
   ps.hidden = (uint32_t)g.H;
   uint32_t parts = 0, rows = 1, want = 0;
@@ -798,7 +903,6 @@ int echo_norm_backward(const echo_norm_desc* d, const void* dz, const void* dh_o
     a.gate_sum = w.gate_sum;
     a.want = want;
     a.scale = d->scale;
-    const bool full = post || d->gate_rows > 0;
     rc = run_norm_backward(a, w.blocks, full, d->dtype, d->stream_dtype, (hipStream_t)stream);
     if (rc) return rc;
   }

@@ -122,6 +122,157 @@ __device__ __forceinline__ void store_n(T* p, int n, const float (&f)[8]) {
     if (i < n) p[i] = from_f32<T>(f[i]);
 }
 
+// A thread's vector of a row in two steps, so that every load of a row is on its
+// way before the first is waited for: fetch() the raw words, unpack() later;
+// neither has a branch, at whose end the loads would be waited for.
+//   kWhole  rows are whole vectors;
+//   kTail   the last vector of a row is short: it is fetched as the row's last
+//           eight elements and moved into place by unpack();
+//   kShort  rows of less than eight elements, fetched one by one.
+// A thread past the row fetches its start and unpacks zeros.
+enum RowEnd { kWhole, kTail, kShort };
+
+template <typename T>
+struct Raw { u32x4 w; };
+template <>
+struct Raw<float> { f32x4 a, b; };
+
+template <typename T>
+__device__ __forceinline__ void keep(Raw<T>& r) { asm volatile("" : "+v"(r.w)); }
+__device__ __forceinline__ void keep(Raw<float>& r) {
+  asm volatile("" : "+v"(r.a));
+  asm volatile("" : "+v"(r.b));
+}
+
+template <bool NT, typename T>
+__device__ __forceinline__ Raw<T> fetch_at(const T* p) {
+  const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
+  if constexpr (NT) return {__builtin_nontemporal_load(q)};
+  else return {*q};
+}
+template <bool NT>
+__device__ __forceinline__ Raw<float> fetch_at(const float* p) {
+  const f32x4_a4* q = reinterpret_cast<const f32x4_a4*>(p);
+  if constexpr (NT) return {__builtin_nontemporal_load(q), __builtin_nontemporal_load(q + 1)};
+  else return {q[0], q[1]};
+}
+__device__ __forceinline__ void unpack_raw(const Raw<float>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = r.a[i];
+    f[4 + i] = r.b[i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack_raw(const Raw<T>& r, float (&f)[8]) {
+  unpack8(r.w, f, T{});
+}
+
+// (the elements past the row are its last one again)
+template <typename T>
+__device__ __forceinline__ Raw<T> fetch_short(const T* row, int H) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = (uint32_t)__builtin_bit_cast(uint16_t, row[min(2 * i, H - 1)]) |
+           (uint32_t)__builtin_bit_cast(uint16_t, row[min(2 * i + 1, H - 1)]) << 16;
+  return {w};
+}
+__device__ __forceinline__ Raw<float> fetch_short(const float* row, int H) {
+  Raw<float> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.a[i] = row[min(i, H - 1)];
+    r.b[i] = row[min(4 + i, H - 1)];
+  }
+  return r;
+}
+
+// where the mask has ones a's bit, else b's (v_bfi_b32)
+__device__ __forceinline__ uint32_t merge(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
+
+// The eight elements moved down by `by` places.  Merged by masks: written as
+// selections, the compiler turns the three steps into a search for each
+// element's index.
+struct MoveDown {
+  uint32_t one, two, four;  // all ones if `by` has that bit
+  __device__ __forceinline__ explicit MoveDown(int by)
+      : one(0u - (by & 1)), two(0u - (by >> 1 & 1)), four(0u - (by >> 2 & 1)) {}
+  __device__ __forceinline__ void operator()(Raw<float>& r) const {
+    uint32_t f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = __float_as_uint(r.a[i]);
+      f[4 + i] = __float_as_uint(r.b[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i) f[i] = merge(one, f[i + 1], f[i]);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) f[i] = merge(two, f[i + 2], f[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = merge(four, f[i + 4], f[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.a[i] = __uint_as_float(f[i]);
+      r.b[i] = __uint_as_float(f[4 + i]);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void operator()(Raw<T>& r) const {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) r.w[i] = merge(two, r.w[i + 1], r.w[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.w[i] = merge(four, r.w[i + 2], r.w[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = __builtin_amdgcn_alignbit(i < 3 ? r.w[i + 1] : 0u, r.w[i], one & 16u);
+  }
+};
+
+// The vector at `col` of a row of H elements, n = H - col of them its own.
+template <RowEnd END>
+struct Place {
+  int from, n;  // where it is fetched
+  MoveDown move;
+  // all ones for the row's own elements, kept as words: as conditions the
+  // eight would not fit the scalar registers
+  uint32_t own[END == kWhole ? 1 : 8];
+  __device__ __forceinline__ Place(int col, int H)
+      : from(END == kTail && H - col > 0 && H - col < 8 ? H - 8 : H - col > 0 ? col : 0),
+        n(H - col),
+        move(H - col > 0 ? col - from : 0) {
+    if constexpr (END != kWhole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        own[i] = i < n ? ~0u : 0u;
+        asm volatile("" : "+v"(own[i]));
+      }
+    }
+  }
+  template <bool NT, typename T>
+  __device__ __forceinline__ Raw<T> fetch(const T* row, int H) const {
+    if constexpr (END == kShort) return fetch_short(row, H);
+    else return fetch_at<NT>(row + from);
+  }
+  // v where element e of the vector is the row's, else 0
+  __device__ __forceinline__ float only(int e, float v) const {
+    if constexpr (END == kWhole) return n > 0 ? v : 0.f;
+    else return __uint_as_float(__float_as_uint(v) & own[e]);
+  }
+  template <typename T>
+  __device__ __forceinline__ void unpack(Raw<T> r, float (&f)[8]) const {
+    if constexpr (END == kTail) move(r);
+    unpack_raw(r, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = only(i, f[i]);
+  }
+  template <bool NT, typename T>
+  __device__ __forceinline__ void store(T* at, const float (&f)[8]) const {  // at: the vector's own place
+    if (n <= 0) return;
+    if constexpr (END == kWhole) store8<NT>(at, f);
+    else store_n<NT>(at, n, f);
+  }
+};
+
 // The same for W = 4 or 8 elements of a 16-bit type.
 template <typename T, int W>
 __device__ __forceinline__ void load_w(const T* p, int n, float (&f)[W]) {
