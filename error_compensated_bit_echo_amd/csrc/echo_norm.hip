@@ -275,6 +275,14 @@ struct NormBackArgs {
   float scale;
 };
 
+// One element of each 128 bytes of a row, a line to a thread: a load for the L2,
+// whose value nobody uses.
+template <typename E>
+__device__ __forceinline__ float touch(const E* row, int H) {
+  const int e = (int)threadIdx.x * (128 / (int)sizeof(E));
+  return e < H ? to_f32(row[e]) : 0.f;
+}
+
 template <int ITEMS>
 __device__ __forceinline__ void zero(float (&v)[ITEMS][8]) {
 #pragma unroll
@@ -312,10 +320,10 @@ __device__ __forceinline__ void flush(float (&acc)[ITEMS][8], const int (&col)[I
 }
 
 // FULL: with a post norm or a gate; else dy = scale dh and only the pre
-// norm's parameters have gradients (fewer accumulators, so more rows in
-// flight).  A workgroup walks `chunk` consecutive rows and keeps the sums over
+// norm's parameters have gradients.  BIAS: with a bias's gradient.  Without them
+// there are fewer accumulators, so more rows in flight.  A workgroup walks `chunk` consecutive rows and keeps the sums over
 // them in registers, so the row data is read once for all outputs.
-template <typename T, typename S, int WAVES, int ITEMS, bool FULL, RowEnd END>
+template <typename T, typename S, int WAVES, int ITEMS, bool FULL, bool BIAS, RowEnd END>
 __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1 ? 3 : 1) void k_norm_backward(
     NormBackArgs a) {
   constexpr bool MANY = WAVES > 1;
@@ -345,7 +353,7 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
     r0 = (int64_t)blockIdx.x * a.chunk;
     r1 = min(r0 + a.chunk, a.tokens);
   }
-  float dw2[ITEMS][8], db2[ITEMS][8], dw1[FULL ? ITEMS : 1][8], db1[FULL ? ITEMS : 1][8],
+  float dw2[ITEMS][8], db2[BIAS ? ITEMS : 1][8], dw1[FULL ? ITEMS : 1][8], db1[FULL && BIAS ? ITEMS : 1][8],
       dg[FULL ? ITEMS : 1][8];
   zero(dw2);
   zero(db2);
@@ -387,6 +395,16 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
       }
       if (FULL && a.rows_per_gate)
         gate.fetch((const T*)a.gate + (int64_t)((uint32_t)row / a.rows_per_gate) * H, at, H);
+      // the next row into the L2 while this one waits at its barriers
+      float ahead[4] = {0.f, 0.f, 0.f, 0.f};
+      if (MANY && row + 1 < s1) {
+        if (a.pre != ECHO_NORM_NONE) {
+          ahead[0] = touch(hp + a.ld_h, H);
+          ahead[1] = touch(dzp + H, H);
+        }
+        if (a.dh_out) ahead[2] = touch(dhp + H, H);
+        if (FULL && a.y) ahead[3] = touch(yp + a.ld_y, H);
+      }
       zero(d);
       if (a.pre != ECHO_NORM_NONE) {
         float sh = 0.f, sg = 0.f;
@@ -400,7 +418,7 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
           for (int e = 0; e < 8; ++e) {
             hat[i][e] = at[i].only(e, (hat[i][e] - mean2) * rstd2);
             dw2[i][e] = fmaf(g[i][e], hat[i][e], dw2[i][e]);
-            db2[i][e] += g[i][e];
+            if constexpr (BIAS) db2[i][e] += g[i][e];
             if (a.w_pre) g[i][e] *= w[e];
             sh = fmaf(g[i][e], hat[i][e], sh);
             sg += g[i][e];
@@ -477,7 +495,7 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               dw1[i][e] = fmaf(d[i][e], y[i][e], dw1[i][e]);
-              db1[i][e] += d[i][e];
+              if constexpr (BIAS) db1[i][e] += d[i][e];
               if (a.w_post) d[i][e] *= w[e];
               sh = fmaf(d[i][e], y[i][e], sh);
               sg += d[i][e];
@@ -499,6 +517,7 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
             for (int e = 0; e < 8; ++e) d[i][e] = rstd1 * ((d[i][e] - sg) - y[i][e] * sh);
         }
       }
+      if constexpr (MANY) asm volatile("" ::"v"(ahead[0]), "v"(ahead[1]), "v"(ahead[2]), "v"(ahead[3]));
       if (a.dy)
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i)
@@ -514,10 +533,12 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
   const int64_t plane = (int64_t)gridDim.x * H;
   float* p = a.part + (int64_t)blockIdx.x * H;
   if (a.want >> kDwPre & 1) flush<float, MANY, ITEMS>(dw2, col, p + kDwPre * plane, H, comb);
-  if (a.want >> kDbPre & 1) flush<float, MANY, ITEMS>(db2, col, p + kDbPre * plane, H, comb);
+  if constexpr (BIAS)
+    if (a.want >> kDbPre & 1) flush<float, MANY, ITEMS>(db2, col, p + kDbPre * plane, H, comb);
   if constexpr (FULL) {
     if (a.want >> kDwPost & 1) flush<float, MANY, ITEMS>(dw1, col, p + kDwPost * plane, H, comb);
-    if (a.want >> kDbPost & 1) flush<float, MANY, ITEMS>(db1, col, p + kDbPost * plane, H, comb);
+    if constexpr (BIAS)
+      if (a.want >> kDbPost & 1) flush<float, MANY, ITEMS>(db1, col, p + kDbPost * plane, H, comb);
     if (a.want >> kDgate & 1) flush<float, MANY, ITEMS>(dg, col, p + kDgate * plane, H, comb);
   }
 }
@@ -689,26 +710,30 @@ int launch_norm(const NormArgs& a, hipStream_t s) {
   return a.hidden % 8 ? launch_norm<T, S, kTail>(a, s) : launch_norm<T, S, kWhole>(a, s);
 }
 
-template <typename T, typename S, bool FULL, RowEnd END>
+template <typename T, typename S, bool FULL, bool BIAS, RowEnd END>
 int launch_norm_backward(const NormBackArgs& a, uint32_t blocks, hipStream_t s) {
   const RowShape r = shape_of(a.hidden, FULL ? kBackFull : kBackPlain);
   const dim3 grid(blocks), block(r.threads);
-  if constexpr (END == kShort) return launch(k_norm_backward<T, S, 1, 1, FULL, END>, grid, block, s, a);
+  if constexpr (END == kShort) return launch(k_norm_backward<T, S, 1, 1, FULL, BIAS, END>, grid, block, s, a);
   else switch (r.waves * 4 + r.items) {
-    case 4 + 1: return launch(k_norm_backward<T, S, 1, 1, FULL, END>, grid, block, s, a);
+    case 4 + 1: return launch(k_norm_backward<T, S, 1, 1, FULL, BIAS, END>, grid, block, s, a);
     case 4 + 2:
-      if constexpr (!FULL) return launch(k_norm_backward<T, S, 1, 2, FULL, END>, grid, block, s, a);
+      if constexpr (!FULL) return launch(k_norm_backward<T, S, 1, 2, FULL, BIAS, END>, grid, block, s, a);
       return ECHO_ERR_SHAPE;
-    case 32 + 1: return launch(k_norm_backward<T, S, 8, 1, FULL, END>, grid, block, s, a);
-    case 64 + 1: return launch(k_norm_backward<T, S, 16, 1, FULL, END>, grid, block, s, a);
-    default: return launch(k_norm_backward<T, S, 16, 2, FULL, END>, grid, block, s, a);
+    case 32 + 1: return launch(k_norm_backward<T, S, 8, 1, FULL, BIAS, END>, grid, block, s, a);
+    case 64 + 1: return launch(k_norm_backward<T, S, 16, 1, FULL, BIAS, END>, grid, block, s, a);
+    default: return launch(k_norm_backward<T, S, 16, 2, FULL, BIAS, END>, grid, block, s, a);
   }
 }
 
 template <typename T, typename S, RowEnd END>
 int launch_norm_backward(const NormBackArgs& a, uint32_t blocks, bool full, hipStream_t s) {
-  return full ? launch_norm_backward<T, S, true, END>(a, blocks, s)
-              : launch_norm_backward<T, S, false, END>(a, blocks, s);
+  const bool bias = a.want >> kDbPre & 1 || a.want >> kDbPost & 1;
+  if (full)
+    return bias ? launch_norm_backward<T, S, true, true, END>(a, blocks, s)
+                : launch_norm_backward<T, S, true, false, END>(a, blocks, s);
+  return bias ? launch_norm_backward<T, S, false, true, END>(a, blocks, s)
+              : launch_norm_backward<T, S, false, false, END>(a, blocks, s);
 }
 
 template <typename T, typename S>
