@@ -10,7 +10,7 @@
 // v_mfma_f32_16x16x32: lane l of a wavefront holds, for row (or column) l % 16
 // of an operand's 16, the eight elements c = 8 (l / 16) .. + 7 of the 32.
 // B's fragment goes into the instruction's first operand, so a lane's four sums
-// are neighbours along j and the epilogue writes vectors along a row of C.
+// are neighbours along j.
 //
 // LDS.  An operand whose rows run along c is stored row by row, 64 elements =
 // eight 16-byte chunks each, and a lane reads its eight elements with one
@@ -157,17 +157,8 @@ __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c, f16_t) {
                                                 c, 0, 0, 0);
 }
 
-// Row of an operand's tile that position rho (0..15) of its 16-row fragment t
-// stands for.  Paired fragments share 32 rows so that a lane's sums of both are
-// eight neighbours; else a fragment is 16 neighbouring rows.
-template <bool PAIRED>
-__device__ __forceinline__ int fragment_row(int t, int rho) {
-  if (PAIRED) return (t >> 1) * 32 + (rho >> 2) * 8 + (t & 1) * 4 + (rho & 3);
-  return t * 16 + rho;
-}
-
 // R rows of an operand by kC of the contraction, NT threads staging it.
-template <bool ACROSS, bool PAIRED, int R, int NT>
+template <bool ACROSS, int R, int NT>
 struct OperandTile {
   static constexpr int kChunks = R * kC / 8;  // 16-byte chunks
   static constexpr int kPer = kChunks / NT;   // of a thread
@@ -176,21 +167,20 @@ struct OperandTile {
 
   static __device__ __forceinline__ int spread(int row) {
     if (ACROSS) return ((row & 3) | (row >> 1 & 4)) & (R / 16 - 1);
-    return PAIRED ? (row & 3) | (row >> 1 & 4) : row & 7;
+    return row & 7;
   }
   // chunk of its row that is stored at place pc of row `row`, and back
   static __device__ __forceinline__ int place(int row, int pc) {
     return ACROSS ? pc ^ (spread(row) << 1) : pc ^ spread(row);
   }
-  // eight elements c = kk*32 + 8 g .. of the rows of fragment t (lane = 16 g + rho)
+  // eight elements c = kk*32 + 8 g .. of row rho of the 16 of fragment t (lane = 16 g + rho)
   static __device__ __forceinline__ s16x8 fragment(const lds_short* lds, int t, int kk, int lane, int base) {
     const int g = lane >> 4, rho = lane & 15;
     if constexpr (!ACROSS) {
-      const int row = base + fragment_row<PAIRED>(t, rho);
+      const int row = base + t * 16 + rho;
       typedef __attribute__((address_space(3))) const s16x8 lds8;
       return *(lds8*)(lds + row * kC + place(row, kk * 4 + g) * 8);
     } else {
-      static_assert(!PAIRED || !ACROSS, "transposed fragments are 16 neighbouring rows");
       typedef __attribute__((address_space(3))) s16x4 lds4;
       s16x4 h[2];
 #pragma unroll

@@ -21,50 +21,57 @@ __device__ __forceinline__ u32x4 raw8(const T* p, int64_t n) {
   return w;
 }
 
-template <int W>
-__device__ __forceinline__ void store_sums(float* p, int n, const float (&v)[W]) {
-  if (n >= W) {
-#pragma unroll
-    for (int e = 0; e < W; e += 4) *(f32x4_a4*)(p + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
-  } else {
-#pragma unroll
-    for (int e = 0; e < W; ++e)
-      if (e < n) p[e] = v[e];
-  }
-}
+// A wavefront's sums to the epilogue, or to a split's partial sums.  Lane 16 g +
+// rho holds, for row rho of each of A's fragments, four neighbours along j of
+// each of B's; written as they are, a store would cover 32 bytes of sixteen
+// rows.  So they go through LDS, which the operands no longer need: one of A's
+// fragments at a time into the wavefront's own part of it, and back with eight
+// neighbours to a lane and whole lines of C to a store.  (The code of the
+// epilogue proper then stands once for all of the wavefront's sums.)
+template <bool GATED, int TJ>
+constexpr int kEpilogueFloats = 16 * (TJ * 16 + 4);  // of a wavefront; rows padded against bank conflicts
 
-// A wavefront's sums to the epilogue, or to a split's partial sums.  Lane
-// 16 g + rho holds row rho of each of A's fragments; along j it holds four sums
-// of one fragment of B or, paired, eight of two.
-template <typename T, bool PAIRED, bool GATED, int TI, int TJ>
-__device__ __forceinline__ void write_tile(const TileArgs& a, const f32x4 (&acc)[TI][TJ], int64_t i0,
+template <typename T, bool GATED, int TI, int TJ>
+__device__ __forceinline__ void write_tile(const TileArgs& a, const f32x4 (&acc)[TI][TJ], float* lds, int64_t i0,
                                            int64_t j0, uint32_t split, int lane) {
+  constexpr int kPitch = TJ * 16 + 4, kOut = GATED ? TJ * 8 : TJ * 16;  // outputs of the wavefront's tile
+  constexpr int kLanes = kOut / 8, kRowsOf = 64 / kLanes;              // lanes to a row, rows to a pass
   const int g = lane >> 4, rho = lane & 15;
   const int64_t cols = GATED ? 2 * a.J : a.J;
+  const int c = lane % kLanes * 8;
+  // gated, runs of 32 gate sums and their 32 up sums alternate
+  const float* const from = lds + lane / kLanes * kPitch + (GATED ? c / 32 * 64 + c % 32 : c);
+  const int64_t col = j0 + c;
+  const int n = (int)min(a.J - col, (int64_t)8);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    const int64_t row = i0 + i * 16 + rho;
-    if (row >= a.I) continue;
-    constexpr int W = PAIRED ? 8 : 4, STEP = GATED ? 4 : PAIRED ? 2 : 1;
 #pragma unroll
-    for (int j = 0; j < TJ; j += STEP) {
-      float v[W], u[W];
+    for (int j = 0; j < TJ; ++j) *(f32x4*)(lds + rho * kPitch + j * 16 + g * 4) = acc[i][j];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int r = 0; r < 16; r += kRowsOf) {
+      const int64_t row = i0 + i * 16 + r + lane / kLanes;
+      float v[8], u[8];
 #pragma unroll
-      for (int e = 0; e < W; ++e) {
-        v[e] = acc[i][j + e / 4][e % 4];
-        u[e] = GATED ? acc[i][(j + 2) % TJ + e / 4][e % 4] : 0.f;
+      for (int e = 0; e < 8; e += 4) {
+        const f32x4 x = *(const f32x4*)(from + r * kPitch + e);
+        const f32x4 y = GATED ? *(const f32x4*)(from + r * kPitch + 32 + e) : x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[e + q] = x[q];
+          u[e + q] = y[q];
+        }
       }
-      const int64_t col = j0 + (GATED ? j * 8 : j * 16) + g * W;
-      if (col >= a.J) continue;
-      const int n = (int)min(a.J - col, (int64_t)W);
+      if (row >= a.I || n <= 0) continue;
       if (a.splits > 1) {
         float* p = a.part + ((int64_t)split * a.I + row) * cols + col;
-        store_sums<W>(p, n, v);
-        if (GATED) store_sums<W>(p + a.J, n, u);
+        store_n<false>(p, n, v);
+        if (GATED) store_n<false>(p + a.J, n, u);
       } else {
-        finish<T, W, GATED>(a, row, col, n, v, u);
+        finish<T, 8, GATED>(a, row, col, n, v, u);
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -73,12 +80,16 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const f32x4 (&acc)
 template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int D>
 __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
-  constexpr bool PAIRED = !TB;
   constexpr int OUT = GATED ? BJ / 2 : BJ;  // outputs of a tile row
-  static_assert(!PAIRED || TJ % (GATED ? 4 : 2) == 0, "fragments of a wavefront");
-  typedef OperandTile<TA, false, BI, NT> A;
-  typedef OperandTile<TB, PAIRED, BJ, NT> B;
-  __shared__ short lds[2][(BI + BJ) * kC];
+  static_assert(!GATED || TJ % 4 == 0, "a gated run is 64 rows of one wavefront");
+  typedef OperandTile<TA, BI, NT> A;
+  typedef OperandTile<TB, BJ, NT> B;
+  constexpr int kEpilogue = kEpilogueFloats<GATED, TJ>;
+  __shared__ union {
+    short stage[2][(BI + BJ) * kC];
+    float sums[WI * WJ][kEpilogue];
+  } mem;
+  auto& lds = mem.stage;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -181,7 +192,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
       }
     }
   }
-  write_tile<T, PAIRED, GATED, TI, TJ>(a, acc, i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
+  write_tile<T, GATED, TI, TJ>(a, acc, mem.sums[wave], i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
 // One 16-byte chunk per lane from memory straight into LDS, the wavefront's 64
@@ -225,15 +236,18 @@ __device__ __forceinline__ u32x4 range_of(const void* p, int64_t bytes) {
 template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S>
 __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
-  constexpr bool PAIRED = !TB;
   constexpr int OUT = GATED ? BJ / 2 : BJ;
-  static_assert(!PAIRED || TJ % (GATED ? 4 : 2) == 0, "fragments of a wavefront");
-  typedef OperandTile<TA, false, BI, NT> A;
-  typedef OperandTile<TB, PAIRED, BJ, NT> B;
+  static_assert(!GATED || TJ % 4 == 0, "a gated run is 64 rows of one wavefront");
+  typedef OperandTile<TA, BI, NT> A;
+  typedef OperandTile<TB, BJ, NT> B;
   constexpr int kStage = (BI + BJ) * kC, kLoads = A::kPer + B::kPer;
   static_assert((S - 1) * kLoads < 64, "loads in flight");
-  __shared__ short lds_mem[S * kStage];
-  lds_short* const lds = (lds_short*)lds_mem;
+  constexpr int kEpilogue = kEpilogueFloats<GATED, TJ>;
+  __shared__ union {
+    short stage[S * kStage];
+    float sums[WI * WJ][kEpilogue];
+  } mem;
+  lds_short* const lds = (lds_short*)mem.stage;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -340,8 +354,11 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
       }
     }
   }
-  dma_wait<0>();  // nothing may arrive in LDS after the workgroup has left it
-  write_tile<T, PAIRED, GATED, TI, TJ>(a, acc, i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
+  // nothing may arrive in LDS that the epilogue uses, or after the workgroup has
+  // left it
+  dma_wait<0>();
+  __syncthreads();
+  write_tile<T, GATED, TI, TJ>(a, acc, mem.sums[wave], i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
 // whether every 16-byte chunk of both operands is aligned and, along c, whole or
