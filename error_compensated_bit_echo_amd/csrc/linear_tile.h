@@ -28,47 +28,61 @@ __device__ __forceinline__ u32x4 raw8(const T* p, int64_t n) {
 // fragments at a time into the wavefront's own part of it, and back with eight
 // neighbours to a lane and whole lines of C to a store.  (The code of the
 // epilogue proper then stands once for all of the wavefront's sums.)
-template <bool GATED, int TJ>
-constexpr int kEpilogueFloats = 16 * (TJ * 16 + 4);  // of a wavefront; rows padded against bank conflicts
+// The groups of four sums of a row are permuted by an exclusive-or with its
+// number against bank conflicts.
+template <int TJ>
+constexpr int kEpilogueFloats = 16 * TJ * 16;  // of a wavefront
 
 template <typename T, bool GATED, int TI, int TJ>
 __device__ __forceinline__ void write_tile(const TileArgs& a, const f32x4 (&acc)[TI][TJ], float* lds, int64_t i0,
                                            int64_t j0, uint32_t split, int lane) {
-  constexpr int kPitch = TJ * 16 + 4, kOut = GATED ? TJ * 8 : TJ * 16;  // outputs of the wavefront's tile
-  constexpr int kLanes = kOut / 8, kRowsOf = 64 / kLanes;              // lanes to a row, rows to a pass
+  constexpr int kPitch = TJ * 16, kOut = GATED ? TJ * 8 : TJ * 16;  // outputs of the wavefront's tile
+  constexpr int kLanes = kOut / 8, kRowsOf = 64 / kLanes;          // lanes to a row, rows to a pass
+  constexpr int kTurn = TJ * 4 < 16 ? TJ * 4 - 1 : 15;             // bits of a row's number that permute
   const int g = lane >> 4, rho = lane & 15;
   const int64_t cols = GATED ? 2 * a.J : a.J;
-  const int c = lane % kLanes * 8;
+  const int c = lane % kLanes * 8, in_pass = lane / kLanes;
   // gated, runs of 32 gate sums and their 32 up sums alternate
-  const float* const from = lds + lane / kLanes * kPitch + (GATED ? c / 32 * 64 + c % 32 : c);
+  const int at = (GATED ? c / 32 * 64 + c % 32 : c) / 4;
   const int64_t col = j0 + c;
   const int n = (int)min(a.J - col, (int64_t)8);
+  auto read = [&](int r, float (&v)[8], float (&u)[8]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const f32x4 x = *(const f32x4*)(lds + r * kPitch + ((at + e) ^ (r & kTurn)) * 4);
+      const f32x4 y = GATED ? *(const f32x4*)(lds + r * kPitch + ((at + 8 + e) ^ (r & kTurn)) * 4) : x;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[e * 4 + q] = x[q];
+        u[e * 4 + q] = y[q];
+      }
+    }
+  };
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) *(f32x4*)(lds + rho * kPitch + j * 16 + g * 4) = acc[i][j];
+    for (int j = 0; j < TJ; ++j) *(f32x4*)(lds + rho * kPitch + ((j * 4 + g) ^ (rho & kTurn)) * 4) = acc[i][j];
     __builtin_amdgcn_wave_barrier();
+    float v[8], u[8];
+    read(in_pass, v, u);
 #pragma unroll 1
     for (int r = 0; r < 16; r += kRowsOf) {
-      const int64_t row = i0 + i * 16 + r + lane / kLanes;
-      float v[8], u[8];
-#pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const f32x4 x = *(const f32x4*)(from + r * kPitch + e);
-        const f32x4 y = GATED ? *(const f32x4*)(from + r * kPitch + 32 + e) : x;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[e + q] = x[q];
-          u[e + q] = y[q];
+      float nv[8], nu[8];  // the next pass's sums on their way
+      read(min(r + kRowsOf, 16 - kRowsOf) + in_pass, nv, nu);
+      const int64_t row = i0 + i * 16 + r + in_pass;
+      if (row < a.I && n > 0) {
+        if (a.splits > 1) {
+          float* p = a.part + ((int64_t)split * a.I + row) * cols + col;
+          store_n<false>(p, n, v);
+          if (GATED) store_n<false>(p + a.J, n, u);
+        } else {
+          finish<T, 8, GATED>(a, row, col, n, v, u);
         }
       }
-      if (row >= a.I || n <= 0) continue;
-      if (a.splits > 1) {
-        float* p = a.part + ((int64_t)split * a.I + row) * cols + col;
-        store_n<false>(p, n, v);
-        if (GATED) store_n<false>(p + a.J, n, u);
-      } else {
-        finish<T, 8, GATED>(a, row, col, n, v, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = nv[e];
+        u[e] = nu[e];
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -84,7 +98,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   static_assert(!GATED || TJ % 4 == 0, "a gated run is 64 rows of one wavefront");
   typedef OperandTile<TA, BI, NT> A;
   typedef OperandTile<TB, BJ, NT> B;
-  constexpr int kEpilogue = kEpilogueFloats<GATED, TJ>;
+  constexpr int kEpilogue = kEpilogueFloats<TJ>;
   __shared__ union {
     short stage[2][(BI + BJ) * kC];
     float sums[WI * WJ][kEpilogue];
@@ -242,7 +256,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   typedef OperandTile<TB, BJ, NT> B;
   constexpr int kStage = (BI + BJ) * kC, kLoads = A::kPer + B::kPer;
   static_assert((S - 1) * kLoads < 64, "loads in flight");
-  constexpr int kEpilogue = kEpilogueFloats<GATED, TJ>;
+  constexpr int kEpilogue = kEpilogueFloats<TJ>;
   __shared__ union {
     short stage[S * kStage];
     float sums[WI * WJ][kEpilogue];
