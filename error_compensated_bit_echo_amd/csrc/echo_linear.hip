@@ -203,15 +203,18 @@ int check_desc(const echo_linear_desc* d, Geometry& g) {
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Which tile, and into how many splits of the contraction.  The estimate of a
-// choice: a compute unit works through n workgroups of `steps` steps, at
-// `step` us a step once it has several to overlap and `alone` us with one (as
-// measured, bf16); splits cost writing and reading their binary32 sums and one
-// more launch.  It is the rule; nothing is tuned to a shape.
-struct TileCost { int bi, bj; float step, alone; };
-constexpr TileCost kChunkedCost[kTileKinds] = {
-    {256, 256, 1.65f, 1.65f}, {256, 128, 1.00f, 1.00f}, {128, 128, 0.50f, 0.62f}, {64, 64, 0.18f, 0.22f}};
+// choice: a compute unit works through n tiles, each at `step` us a step and
+// `over` us from its last step to the next tile's first, and a tile takes at
+// least `alone` us a step, when it has no other to overlap with (as measured,
+// bf16); splits cost writing and reading their binary32 sums and one more
+// launch.  It is the rule; nothing is tuned to a shape.
+struct TileCost { int bi, bj; float step, over, alone; };
+constexpr TileCost kChunkedCost[kTileKinds] = {{256, 256, 1.45f, 8.5f, 1.45f},
+                                               {256, 128, 0.88f, 4.5f, 0.88f},
+                                               {128, 128, 0.45f, 1.8f, 0.62f},
+                                               {64, 64, 0.185f, 0.8f, 0.22f}};
 constexpr TileCost kStagedCost[kTileKinds] = {
-    {0, 0, 0, 0}, {0, 0, 0, 0}, {128, 128, 1.00f, 1.10f}, {64, 64, 0.38f, 0.50f}};
+    {0, 0, 0, 0, 0}, {0, 0, 0, 0, 0}, {128, 128, 1.00f, 2.0f, 1.10f}, {64, 64, 0.38f, 1.0f, 0.50f}};
 constexpr int64_t kMostPart = INT64_C(256) << 20;  // bytes of partial sums
 
 struct Plan { int tile; int64_t splits, chunk, part_bytes; double us; };
@@ -229,8 +232,8 @@ Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
       const double bytes = splits > 1 ? 4.0 * (double)I * (double)cols * (double)splits : 0.0;
       if (bytes > (double)kMostPart) break;
       const double per_cu = ceil(tiles * (double)splits / 256.0);
-      const double busy = per_cu * k.step > k.alone ? per_cu * k.step : k.alone;
-      const double us = (double)each * busy + (splits > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
+      const double shared = per_cu * ((double)each * k.step + k.over), lone = (double)each * k.alone + k.over;
+      const double us = (shared > lone ? shared : lone) + (splits > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
       if (us < best.us) best = {t, splits, each * kC, splits > 1 ? (int64_t)bytes : 0, us};
     }
   }

@@ -339,19 +339,39 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const lds_short* la) {
+  // One step; `load` issues the loads of the step S - 1 ahead, behind this step's
+  // first reads of LDS rather than before them (8192 x 8192 x 4096: 423 -> 399
+  // us).  With both operands read across c the reads of the step's second half
+  // are also spread over the products of its first (413 -> 393 us; along c that
+  // costs as much, 399 -> 417).
+  auto multiply = [&](const lds_short* la, auto load) {
     const lds_short* lb = la + BI * kC;
+    static_assert(kC == 64, "two halves");
+    s16x8 fa[2][TI], fb[2][TJ];
+    auto read = [&](int kk) {
 #pragma unroll
-    for (int kk = 0; kk < kC / 32; ++kk) {
-      s16x8 fa[TI], fb[TJ];
+      for (int j = 0; j < TJ; ++j) fb[kk][j] = B::fragment(lb, j, kk, lane, wj);
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) fb[j] = B::fragment(lb, j, kk, lane, wj);
+      for (int i = 0; i < TI; ++i) fa[kk][i] = A::fragment(la, i, kk, lane, wi);
+    };
+    if constexpr (GATED) load();
+    read(0);
+    if constexpr (!GATED) load();
+    if constexpr (TA && TB) read(1);
 #pragma unroll
-      for (int i = 0; i < TI; ++i) fa[i] = A::fragment(la, i, kk, lane, wi);
+    for (int kk = 0; kk < 2; ++kk) {
+      if (kk == 1 && !(TA && TB)) read(1);
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[j], fa[i], acc[i][j], T{});
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[kk][j], fa[kk][i], acc[i][j], T{});
+    }
+    if constexpr (TA && TB) {
+#pragma unroll
+      for (int q = 0; q < TI + TJ; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read of LDS,
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // two products
+      }
     }
   };
 
@@ -363,8 +383,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
       if (s + u < steps) {
         dma_wait<(S - 2) * kLoads>();
         __syncthreads();
-        stage(lds + (u + S - 1) % S * kStage, s + u + S - 1);
-        multiply(lds + u * kStage);
+        multiply(lds + u * kStage, [&] { stage(lds + (u + S - 1) % S * kStage, s + u + S - 1); });
       }
     }
   }
