@@ -18,72 +18,89 @@ namespace {
 // ---- dp: the gradient of the sums before the activation ---------------------------
 // One pass over dout and p that writes dp, rounded, for both products, and sums
 // its columns in binary32 for the bias.  A thread holds 8 columns and walks
-// down the rows of its workgroup's run; 32 threads lie side by side, 8 above
-// each other.  Bound by HBM: 2 bytes in per dout and p element, 2 out.
+// down the rows of its workgroup's run; `wide` threads lie side by side, 256 /
+// wide above each other.  Bound by HBM: 2 bytes in per dout and p element, 2 out.
 struct SlopeArgs {
   const void *dout;
   const void* p;  // nullable: no activation, dp is a copy of dout
   void* dp;       // nullable: dp is dout itself; rows filled up with zeros to ld_dp
-  float* part;  // nullable: [runs][columns of dp] sums
+  float* part;    // nullable: [runs][columns of dp] sums
   int64_t m, n, ld_out, ld_dp, run;
-  int32_t act, gated;
+  int32_t act, gated, wide;  // wide: 8, 16 or 32
 };
 
-template <typename T>
+template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
-  __shared__ float lds[2][8][256 + 8];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 256 + tx * 8;
+  __shared__ float lds[GATED ? 2 : 1][256 * 8 + 32 * 8];
+  const int tx = threadIdx.x & (a.wide - 1), ty = threadIdx.x / a.wide, high = 256 / a.wide;
+  const int64_t col = ((int64_t)blockIdx.x * a.wide + tx) * 8;
   const int64_t r0 = (int64_t)blockIdx.y * a.run, r1 = min(r0 + a.run, a.m);
   const int n = (int)min(a.n - col, (int64_t)9);  // 8 or less: the row's last vector
-  const int64_t cols = a.gated ? 2 * a.n : a.n;
+  const int64_t cols = GATED ? 2 * a.n : a.n;
   float sg[8], su[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sg[e] = su[e] = 0.f;
-  if (n > 0)
-    for (int64_t r = r0 + ty; r < r1; r += 8) {
-      float d[8], p[8], u[8];
-      load_n<false>((const T*)a.dout + r * a.ld_out + col, n, d);
-      if (a.p) {
-        load_n<true>((const T*)a.p + r * cols + col, n, p);
-        if (a.gated) load_n<true>((const T*)a.p + r * cols + a.n + col, n, u);
+  auto row = [&](int64_t r, float (&d)[8], float (&p)[8], float (&u)[8]) {
+    if (a.p)
+      with_act(a.act, [&](auto act) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float v, slope;
-          act_slope(p[e], a.act, v, slope);
-          if (a.gated) {
+          act_slope<decltype(act)::value>(p[e], v, slope);
+          if (GATED) {
             p[e] = d[e] * v;
             d[e] *= u[e];
           }
           d[e] *= slope;
         }
-      }
-      if (a.dp) {
-        T* dp = (T*)a.dp + r * a.ld_dp;
-        store_n<false>(dp + col, n, d);
-        if (a.gated) store_n<false>(dp + a.n + col, n, p);
-        if (n <= 8)
-          for (int64_t c = cols; c < a.ld_dp; ++c) dp[c] = from_f32<T>(0.f);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sg[e] += d[e];
-        if (a.gated) su[e] += p[e];
-      }
+      });
+    if (a.dp) {
+      T* dp = (T*)a.dp + r * a.ld_dp;
+      store_n<false>(dp + col, n, d);
+      if (GATED) store_n<false>(dp + a.n + col, n, p);
+      if (n <= 8)
+        for (int64_t c = cols; c < a.ld_dp; ++c) dp[c] = from_f32<T>(0.f);
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      sg[e] += d[e];
+      if (GATED) su[e] += p[e];
+    }
+  };
+  auto load = [&](int64_t r, float (&d)[8], float (&p)[8], float (&u)[8]) {
+    load_n<true>((const T*)a.dout + r * a.ld_out + col, n, d);
+    if (!a.p) return;
+    load_n<true>((const T*)a.p + r * cols + col, n, p);
+    if (GATED) load_n<true>((const T*)a.p + r * cols + a.n + col, n, u);
+  };
+  if (n > 0) {
+    float d[2][8], p[2][8], u[2][8];
+    int64_t r = r0 + ty;
+    for (; r + high < r1; r += 2 * high) {  // two rows on their way at once
+      load(r, d[0], p[0], u[0]);
+      load(r + high, d[1], p[1], u[1]);
+      row(r, d[0], p[0], u[0]);
+      row(r + high, d[1], p[1], u[1]);
+    }
+    if (r < r1) {
+      load(r, d[0], p[0], u[0]);
+      row(r, d[0], p[0], u[0]);
+    }
+  }
   if (!a.part) return;
+  const int pitch = a.wide * 8 + 8;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    lds[0][ty][tx * 8 + e] = sg[e];
-    if (a.gated) lds[1][ty][tx * 8 + e] = su[e];
+    lds[0][ty * pitch + tx * 8 + e] = sg[e];
+    if constexpr (GATED) lds[1][ty * pitch + tx * 8 + e] = su[e];
   }
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c < a.n)
-    for (int h = 0; h <= a.gated; ++h) {
-      float s = lds[h][0][threadIdx.x];
+  const int64_t c = (int64_t)blockIdx.x * a.wide * 8 + threadIdx.x;
+  if ((int)threadIdx.x < a.wide * 8 && c < a.n)
 #pragma unroll
-      for (int k = 1; k < 8; ++k) s += lds[h][k][threadIdx.x];
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+      float s = lds[h][threadIdx.x];
+      for (int k = 1; k < high; ++k) s += lds[h][k * pitch + threadIdx.x];
       a.part[(int64_t)blockIdx.y * cols + h * a.n + c] = s;
     }
 }
@@ -129,7 +146,13 @@ __global__ __launch_bounds__(1024) void k_run_sum(RunSumArgs a) {
   const int64_t col = (int64_t)blockIdx.x * 32 + c;
   float s = 0.f;
   if (col < a.cols)
-    for (uint32_t r = k; r < a.runs; r += 32) s += a.part[r * a.cols + col];
+    for (uint32_t r = k; r < a.runs; r += 4 * 32) {  // four loads on their way at once
+      float v[4];
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) v[e] = r + e * 32 < a.runs ? a.part[(r + e * 32) * a.cols + col] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += v[e];
+    }
   lds[k][c] = s;
   __syncthreads();
   if (k == 0 && col < a.cols) {
@@ -302,6 +325,7 @@ void apply(const Plan& p, void* part, TileArgs& a) {
 // each run of rows, and the splits' sums.
 struct BackPlan {
   bool copies;
+  int32_t wide;
   int64_t ld_dp, dp_bytes, x_bytes, w_bytes, run, runs, bias_bytes, split_bytes;
   int64_t bytes() const { return dp_bytes + x_bytes + w_bytes + bias_bytes + split_bytes; }
 };
@@ -325,10 +349,13 @@ BackPlan plan_back(const echo_linear_desc* d, const Geometry& g) {
     b.ld_dp = round_up(g.rows, 8);
     b.dp_bytes = round_up(g.m * b.ld_dp * 2, 16);
   }
-  const int64_t strips = (g.n + 255) / 256;
+  // the widest strip of columns that wastes the fewest threads
+  b.wide = 32;
+  for (const int wide : {16, 8})
+    if (round_up(g.n, wide * 8) < round_up(g.n, b.wide * 8)) b.wide = wide;
+  const int64_t strips = (g.n + b.wide * 8 - 1) / (b.wide * 8);
   const int64_t most = strips ? (2048 + strips - 1) / strips : 1;  // workgroups along the rows
-  b.run = round_up((g.m + most - 1) / most, 8);
-  if (b.run < 32) b.run = 32;
+  b.run = round_up(g.m > 0 ? (g.m + most - 1) / most : 1, 512 / b.wide);
   b.runs = (g.m + b.run - 1) / b.run;
   b.bias_bytes = round_up(b.runs * g.rows * 4, 16);
   const int64_t dx = part_bytes(g.m, g.k, g.rows), dw = part_bytes(g.rows, g.k, g.m);
@@ -467,8 +494,12 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
     a.run = b.run;
     a.act = d->act;
     a.gated = d->gated;
-    const dim3 grid((uint32_t)((g.n + 255) / 256), (uint32_t)b.runs), block(256);
-    rc = bf16 ? launch(k_slope<bf16_t>, grid, block, s, a) : launch(k_slope<f16_t>, grid, block, s, a);
+    a.wide = b.wide;
+    const dim3 grid((uint32_t)((g.n + b.wide * 8 - 1) / (b.wide * 8)), (uint32_t)b.runs), block(256);
+    if (d->gated)
+      rc = bf16 ? launch(k_slope<bf16_t, true>, grid, block, s, a) : launch(k_slope<f16_t, true>, grid, block, s, a);
+    else
+      rc = bf16 ? launch(k_slope<bf16_t, false>, grid, block, s, a) : launch(k_slope<f16_t, false>, grid, block, s, a);
     if (rc) return rc;
   }
   if (dbias && g.rows > 0) {

@@ -23,6 +23,7 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "echo_layer.h"
 #include "layer_device.h"
@@ -66,43 +67,39 @@ __device__ __forceinline__ float gelu_tanh_gate(float x) {
   return sigmoid(1.59576912f * fmaf(0.044715f * x * x, x, x));
 }
 
-__device__ __forceinline__ float act_of(float p, int act) {
-  switch (act) {
-    case ECHO_ACT_RELU: return p <= 0.f ? 0.f : p;
-    case ECHO_ACT_GELU: return p * normal_cdf(p);
-    case ECHO_ACT_GELU_TANH: return p * gelu_tanh_gate(p);
-    case ECHO_ACT_SILU: return p * sigmoid(p);
-    default: return p;
+// value and slope of each activation
+template <int ACT>
+__device__ __forceinline__ void act_slope(float p, float& v, float& d) {
+  if constexpr (ACT == ECHO_ACT_RELU) {
+    v = p <= 0.f ? 0.f : p;
+    d = p > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == ECHO_ACT_GELU) {
+    const float c = normal_cdf(p);
+    v = p * c;
+    d = fmaf(p * 0.39894228f, exp_fast(-0.5f * p * p), c);
+  } else if constexpr (ACT == ECHO_ACT_GELU_TANH) {
+    const float s = gelu_tanh_gate(p);
+    v = p * s;
+    d = fmaf(v * (1.f - s), 1.59576912f * fmaf(0.134145f, p * p, 1.f), s);
+  } else if constexpr (ACT == ECHO_ACT_SILU) {
+    const float s = sigmoid(p);
+    v = p * s;
+    d = fmaf(v, 1.f - s, s);
+  } else {
+    v = p;
+    d = 1.f;
   }
 }
-// value and slope
-__device__ __forceinline__ void act_slope(float p, int act, float& v, float& d) {
+
+// f<ACT>() for the activation a call names: one branch for a whole vector
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
-    case ECHO_ACT_RELU:
-      v = p <= 0.f ? 0.f : p;
-      d = p > 0.f ? 1.f : 0.f;
-      return;
-    case ECHO_ACT_GELU: {
-      const float c = normal_cdf(p);
-      v = p * c;
-      d = fmaf(p * 0.39894228f, exp_fast(-0.5f * p * p), c);
-      return;
-    }
-    case ECHO_ACT_GELU_TANH: {
-      const float s = gelu_tanh_gate(p);
-      v = p * s;
-      d = fmaf(v * (1.f - s), 1.59576912f * fmaf(0.134145f, p * p, 1.f), s);
-      return;
-    }
-    case ECHO_ACT_SILU: {
-      const float s = sigmoid(p);
-      v = p * s;
-      d = fmaf(v, 1.f - s, s);
-      return;
-    }
-    default:
-      v = p;
-      d = 1.f;
+    case ECHO_ACT_RELU: return f(std::integral_constant<int, ECHO_ACT_RELU>{});
+    case ECHO_ACT_GELU: return f(std::integral_constant<int, ECHO_ACT_GELU>{});
+    case ECHO_ACT_GELU_TANH: return f(std::integral_constant<int, ECHO_ACT_GELU_TANH>{});
+    case ECHO_ACT_SILU: return f(std::integral_constant<int, ECHO_ACT_SILU>{});
+    default: return f(std::integral_constant<int, ECHO_ACT_NONE>{});
   }
 }
 
@@ -129,10 +126,13 @@ __device__ __forceinline__ void finish(const TileArgs& a, int64_t i, int64_t j, 
     store_w<T, W>(p, n, g);
     if constexpr (GATED) store_w<T, W>(p + a.J, n, u);
   }
-  if (GATED || a.act != ECHO_ACT_NONE) {
+  with_act(a.act, [&](auto act) {
 #pragma unroll
-    for (int e = 0; e < W; ++e) g[e] = act_of(g[e], a.act);
-  }
+    for (int e = 0; e < W; ++e) {
+      float slope;
+      act_slope<decltype(act)::value>(g[e], g[e], slope);
+    }
+  });
   if constexpr (GATED) {
 #pragma unroll
     for (int e = 0; e < W; ++e) g[e] *= u[e];

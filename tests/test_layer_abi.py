@@ -144,6 +144,17 @@ def test_linear_backward_rejections():
     assert linb(ldesc(act=4), p=7 * A, dx=6 * A) == -6                 # over the workspace
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_workspace_queries_take_empty_and_odd_shapes(act, gated):
+    for m in (0, 1, 16, 17, 1000, 1 << 20):
+        for n in (0, 1, 7, 8, 384, 1793):
+            for k in (0, 1, 7, 64, 1001):
+                f = B.echo_linear_workspace(m, n, k, act=act, gated=gated)
+                b = B.echo_linear_backward_workspace(m, n, k, act=act, gated=gated)
+                assert f >= 0 and b >= 0 and f % 16 == 0 and b % 16 == 0, (m, n, k)
+
+
 def test_binding_refuses_before_the_library():
     t = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU tensor"):
