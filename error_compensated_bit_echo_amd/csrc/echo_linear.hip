@@ -29,7 +29,9 @@ struct SlopeArgs {
   int32_t act, gated, wide;  // wide: 8, 16 or 32
 };
 
-template <typename T, bool GATED>
+// WHOLE: rows are whole vectors, so that two rows' loads are on their way at once
+// without a branch at whose end they would be waited for.
+template <typename T, bool GATED, bool WHOLE>
 __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
   __shared__ float lds[GATED ? 2 : 1][256 * 8 + 32 * 8];
   const int tx = threadIdx.x & (a.wide - 1), ty = threadIdx.x / a.wide, high = 256 / a.wide;
@@ -67,24 +69,35 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
       if (GATED) su[e] += p[e];
     }
   };
-  auto load = [&](int64_t r, float (&d)[8], float (&p)[8], float (&u)[8]) {
-    load_n<true>((const T*)a.dout + r * a.ld_out + col, n, d);
-    if (!a.p) return;
-    load_n<true>((const T*)a.p + r * cols + col, n, p);
-    if (GATED) load_n<true>((const T*)a.p + r * cols + a.n + col, n, u);
-  };
-  if (n > 0) {
-    float d[2][8], p[2][8], u[2][8];
-    int64_t r = r0 + ty;
-    for (; r + high < r1; r += 2 * high) {  // two rows on their way at once
-      load(r, d[0], p[0], u[0]);
-      load(r + high, d[1], p[1], u[1]);
-      row(r, d[0], p[0], u[0]);
-      row(r + high, d[1], p[1], u[1]);
+  if (WHOLE && n > 0) {
+    for (int64_t r = r0 + ty; r < r1; r += 2 * high) {
+      Raw<T> d[2], p[2], u[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // past the end the last row once more
+        const int64_t at = min(r + k * high, r1 - 1);
+        d[k] = fetch_at<true>((const T*)a.dout + at * a.ld_out + col);
+        if (a.p) p[k] = fetch_at<true>((const T*)a.p + at * cols + col);
+        if (GATED && a.p) u[k] = fetch_at<true>((const T*)a.p + at * cols + a.n + col);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (r + k * high >= r1) continue;
+        float fd[8], fp[8], fu[8];
+        unpack_raw(d[k], fd);
+        if (a.p) unpack_raw(p[k], fp);
+        if (GATED && a.p) unpack_raw(u[k], fu);
+        row(r + k * high, fd, fp, fu);
+      }
     }
-    if (r < r1) {
-      load(r, d[0], p[0], u[0]);
-      row(r, d[0], p[0], u[0]);
+  } else if (n > 0) {
+    for (int64_t r = r0 + ty; r < r1; r += high) {
+      float d[8], p[8], u[8];
+      load_n<true>((const T*)a.dout + r * a.ld_out + col, n, d);
+      if (a.p) {
+        load_n<true>((const T*)a.p + r * cols + col, n, p);
+        if (GATED) load_n<true>((const T*)a.p + r * cols + a.n + col, n, u);
+      }
+      row(r, d, p, u);
     }
   }
   if (!a.part) return;
@@ -314,6 +327,12 @@ int run_join(const TileArgs& a, int32_t dtype, hipStream_t s) {
                             : launch(k_join<f16_t, GATED>, grid, block, s, a);
 }
 
+template <typename T, bool GATED>
+int run_slope(const SlopeArgs& a, dim3 grid, dim3 block, hipStream_t s) {
+  return a.n % 8 ? launch(k_slope<T, GATED, false>, grid, block, s, a)
+                 : launch(k_slope<T, GATED, true>, grid, block, s, a);
+}
+
 void apply(const Plan& p, void* part, TileArgs& a) {
   a.splits = (uint32_t)p.splits;
   a.chunk = p.chunk;
@@ -497,9 +516,9 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
     a.wide = b.wide;
     const dim3 grid((uint32_t)((g.n + b.wide * 8 - 1) / (b.wide * 8)), (uint32_t)b.runs), block(256);
     if (d->gated)
-      rc = bf16 ? launch(k_slope<bf16_t, true>, grid, block, s, a) : launch(k_slope<f16_t, true>, grid, block, s, a);
+      rc = bf16 ? run_slope<bf16_t, true>(a, grid, block, s) : run_slope<f16_t, true>(a, grid, block, s);
     else
-      rc = bf16 ? launch(k_slope<bf16_t, false>, grid, block, s, a) : launch(k_slope<f16_t, false>, grid, block, s, a);
+      rc = bf16 ? run_slope<bf16_t, false>(a, grid, block, s) : run_slope<f16_t, false>(a, grid, block, s);
     if (rc) return rc;
   }
   if (dbias && g.rows > 0) {
