@@ -10,7 +10,7 @@ static int product(const TileArgs& a, int tile, hipStream_t s) {
       case kTile256: return launch_tile<T, true, true, 256, 256, 2, 4, false, 2>(a, s);
       case kTile256x128: return launch_tile<T, true, true, 256, 128, 4, 2, false, 3>(a, s);
       case kTile128: return launch_tile<T, true, true, 128, 128, 2, 2, false, 2>(a, s);
-      default: return launch_tile<T, true, true, 64, 64, 2, 2, false, 4>(a, s);
+      default: return launch_tile<T, true, true, 64, 64, 2, 2, false, 4, 2>(a, s);
     }
   }
   if (tile != kTile64) return launch_tile<T, true, true, 128, 128, 2, 2, false, -2>(a, s);

@@ -11,7 +11,7 @@ static int forward(const TileArgs& a, int tile, hipStream_t s) {
       case kTile256: return launch_tile<T, false, false, 256, 256, 4, 2, GATED, 2>(a, s);
       case kTile256x128: return launch_tile<T, false, false, 256, 128, 4, 2, GATED, 3>(a, s);
       case kTile128: return launch_tile<T, false, false, 128, 128, 2, 2, GATED, 2>(a, s);
-      default: return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, 4>(a, s);
+      default: return launch_tile<T, false, false, 64, 64, SI, SJ, GATED, 4, 2>(a, s);
     }
   }
   if (tile != kTile64) return launch_tile<T, false, false, 128, 128, 2, 2, GATED, -2>(a, s);

@@ -247,9 +247,12 @@ __device__ __forceinline__ u32x4 range_of(const void* p, int64_t bytes) {
 // arrive.  A step waits for its own stage only, and its one barrier says both
 // that every wavefront's part of the stage is there and that the stage before,
 // whose place the next loads take, has been read.
-template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S>
-__global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
-  constexpr int NT = 64 * WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
+// WK = 2: the two halves of a step's contraction go to two sets of wavefronts,
+// whose sums are added at the end: a small tile's step is bound by the latency of
+// one wavefront's reads and products, not by their number.
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S, int WK>
+__global__ __launch_bounds__(64 * WI * WJ * WK, 2) void k_tile_dma(TileArgs a) {
+  constexpr int NT = 64 * WI * WJ * WK, TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr int OUT = GATED ? BJ / 2 : BJ;
   static_assert(!GATED || TJ % 4 == 0, "a gated run is 64 rows of one wavefront");
   typedef OperandTile<TA, BI, NT> A;
@@ -259,13 +262,17 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   constexpr int kEpilogue = kEpilogueFloats<TJ>;
   __shared__ union {
     short stage[S * kStage];
-    float sums[WI * WJ][kEpilogue];
+    struct {
+      float sums[WI * WJ][kEpilogue];
+      f32x4 halves[WK == 2 ? WI * WJ : 1][TI * TJ][64];
+    };
   } mem;
   lds_short* const lds = (lds_short*)mem.stage;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+  const int own = wave % (WI * WJ), half = wave / (WI * WJ);  // half: 0 where WK is 1
+  const int wi = own % WI * (BI / WI), wj = own / WI * (BJ / WJ);
   const uint32_t tiles = a.tiles_i * a.tiles_j;
   uint32_t ti, tj, split = 0;
   if (a.splits > 1) split = blockIdx.x / tiles;
@@ -354,6 +361,18 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
 #pragma unroll
       for (int i = 0; i < TI; ++i) fa[kk][i] = A::fragment(la, i, kk, lane, wi);
     };
+    if constexpr (WK == 2) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) fb[0][j] = B::fragment(lb, j, half, lane, wj);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) fa[0][i] = A::fragment(la, i, half, lane, wi);
+      load();
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[0][j], fa[0][i], acc[i][j], T{});
+      return;
+    }
     if constexpr (GATED) load();
     read(0);
     if constexpr (!GATED) load();
@@ -391,7 +410,21 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile_dma(TileArgs a) {
   // left it
   dma_wait<0>();
   __syncthreads();
-  write_tile<T, GATED, TI, TJ>(a, acc, mem.sums[wave], i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
+  if constexpr (WK == 2) {
+    f32x4* const other = mem.halves[own][0] + lane;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        if (half) other[(i * TJ + j) * 64] = acc[i][j];
+    __syncthreads();
+    if (half) return;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] += other[(i * TJ + j) * 64];
+  }
+  write_tile<T, GATED, TI, TJ>(a, acc, mem.sums[own], i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
 // whether every 16-byte chunk of both operands is aligned and, along c, whole or
@@ -403,17 +436,17 @@ bool chunked(const TileArgs& a) {
 }
 
 // S: stages fed by direct loads, or, negative, steps loaded ahead through registers
-template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S>
+template <typename T, bool TA, bool TB, int BI, int BJ, int WI, int WJ, bool GATED, int S, int WK = 1>
 int launch_tile(TileArgs a, hipStream_t s) {
   const int64_t out = GATED ? BJ / 2 : BJ;
   const int64_t ti = (a.I + BI - 1) / BI, tj = (a.J + out - 1) / out;
-  constexpr int NT = 64 * WI * WJ;
+  constexpr int NT = 64 * WI * WJ * WK;
   if (ti * tj == 0) return ECHO_SUCCESS;
   if (ti * tj > (int64_t)(0xFFFFFFFFu / NT) / a.splits) return ECHO_ERR_SHAPE;
   a.tiles_i = (uint32_t)ti;
   a.tiles_j = (uint32_t)tj;
   const dim3 grid(a.tiles_i * a.tiles_j * a.splits);
-  if constexpr (S > 0) return launch(k_tile_dma<T, TA, TB, BI, BJ, WI, WJ, GATED, S>, grid, dim3(NT), s, a);
+  if constexpr (S > 0) return launch(k_tile_dma<T, TA, TB, BI, BJ, WI, WJ, GATED, S, WK>, grid, dim3(NT), s, a);
   else return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED, -S>, grid, dim3(NT), s, a);
 }
 
