@@ -261,16 +261,19 @@ Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
   for (int t = 0; t < kTileKinds; ++t) {
     const TileCost& k = is_chunked ? kChunkedCost[t] : kStagedCost[t];
     if (k.bi == 0) continue;
-    const double tiles = (double)((I + k.bi - 1) / k.bi) * (double)((cols + k.bj - 1) / k.bj);
-    for (int64_t splits = 1; splits <= 32; ++splits) {
+    const int64_t tiles = ((I + k.bi - 1) / k.bi) * ((cols + k.bj - 1) / k.bj);
+    // at least four steps to a split, and no more than four rounds of workgroups
+    const int64_t room = tiles > 0 ? 1024 / tiles : 1, deep = steps / 4;
+    const int64_t most = room < deep ? (room < 32 ? room : 32) : (deep < 32 ? deep : 32);
+    for (int64_t splits = 1; splits <= most || splits == 1; splits += splits / 4 + 1) {
       const int64_t each = (steps + splits - 1) / splits;
-      if (splits > 1 && (each < 4 || (steps + each - 1) / each != splits)) continue;
-      const double bytes = splits > 1 ? 4.0 * (double)I * (double)cols * (double)splits : 0.0;
+      const int64_t real = each > 0 ? (steps + each - 1) / each : 1;  // splits that have steps
+      const double bytes = real > 1 ? 4.0 * (double)I * (double)cols * (double)real : 0.0;
       if (bytes > (double)kMostPart) break;
-      const double per_cu = ceil(tiles * (double)splits / 256.0);
+      const double per_cu = (double)((tiles * real + 255) / 256);
       const double shared = per_cu * ((double)each * k.step + k.over), lone = (double)each * k.alone + k.over;
-      const double us = (shared > lone ? shared : lone) + (splits > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
-      if (us < best.us) best = {t, splits, each * kC, splits > 1 ? (int64_t)bytes : 0, us};
+      const double us = (shared > lone ? shared : lone) + (real > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
+      if (us < best.us) best = {t, real > 0 ? real : 1, each * kC, real > 1 ? (int64_t)bytes : 0, us};
     }
   }
   return best;
