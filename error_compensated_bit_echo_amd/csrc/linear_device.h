@@ -215,11 +215,15 @@ struct OperandTile {
 // of tiles, and runs go over a band of tile rows before the next tile column, so
 // that the 32 tiles in flight on an XCD share operands in its L2: 8 rows by 4
 // columns, or, where there are fewer columns, all of them by as many rows
-// (131072 x 1792 x 4096, seven columns: bands of 4 rows 1541 us, of 8 1580).
+// (131072 x 1792 x 4096, seven columns: bands of 4 rows 1541 us, of 8 1580).  A
+// split's tiles follow each other, so that its part of both operands is read by
+// one XCD or two.
 __device__ __forceinline__ void tile_of(uint32_t b, uint32_t nb, uint32_t tiles_i, uint32_t tiles_j,
-                                        uint32_t& ti, uint32_t& tj) {
-  const uint32_t xcd = b % 8, k = b / 8, per = nb / 8, extra = nb % 8;
-  const uint32_t t = xcd * per + (xcd < extra ? xcd : extra) + k;
+                                        uint32_t& ti, uint32_t& tj, uint32_t& split) {
+  const uint32_t xcd = b % 8, k = b / 8, per = nb / 8, extra = nb % 8, tiles = tiles_i * tiles_j;
+  uint32_t t = xcd * per + (xcd < extra ? xcd : extra) + k;
+  split = tiles == nb ? 0 : t / tiles;
+  t -= split * tiles;
   const uint32_t rows_of = tiles_j >= 8 ? 8 : 32 / tiles_j;
   const uint32_t band = t / (rows_of * tiles_j), first = band * rows_of;
   const uint32_t rows = min(rows_of, tiles_i - first), r = t - first * tiles_j;

@@ -108,10 +108,8 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
-  const uint32_t tiles = a.tiles_i * a.tiles_j;
-  uint32_t ti, tj, split = 0;
-  if (a.splits > 1) split = blockIdx.x / tiles;
-  tile_of(blockIdx.x - split * tiles, tiles, a.tiles_i, a.tiles_j, ti, tj);
+  uint32_t ti, tj, split;
+  tile_of(blockIdx.x, gridDim.x, a.tiles_i, a.tiles_j, ti, tj, split);
   const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * OUT;
   const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
   const int steps = (int)((c1 - c0 + kC - 1) / kC);
@@ -273,10 +271,8 @@ __global__ __launch_bounds__(64 * WI * WJ * WK, 2) void k_tile_dma(TileArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int own = wave % (WI * WJ), half = wave / (WI * WJ);  // half: 0 where WK is 1
   const int wi = own % WI * (BI / WI), wj = own / WI * (BJ / WJ);
-  const uint32_t tiles = a.tiles_i * a.tiles_j;
-  uint32_t ti, tj, split = 0;
-  if (a.splits > 1) split = blockIdx.x / tiles;
-  tile_of(blockIdx.x - split * tiles, tiles, a.tiles_i, a.tiles_j, ti, tj);
+  uint32_t ti, tj, split;
+  tile_of(blockIdx.x, gridDim.x, a.tiles_i, a.tiles_j, ti, tj, split);
   const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * OUT;
   const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
   const int steps = (int)((c1 - c0 + kC - 1) / kC);
