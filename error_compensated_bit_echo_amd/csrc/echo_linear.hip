@@ -265,7 +265,7 @@ Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
     // at least four steps to a split, and no more than four rounds of workgroups
     const int64_t room = tiles > 0 ? 1024 / tiles : 1, deep = steps / 4;
     const int64_t most = room < deep ? (room < 32 ? room : 32) : (deep < 32 ? deep : 32);
-    for (int64_t splits = 1; splits <= most || splits == 1; splits += splits / 4 + 1) {
+    for (int64_t splits = 1; splits <= most || splits == 1; splits += splits < 16 ? 1 : 4) {
       const int64_t each = (steps + splits - 1) / splits;
       const int64_t real = each > 0 ? (steps + each - 1) / each : 1;  // splits that have steps
       const double bytes = real > 1 ? 4.0 * (double)I * (double)cols * (double)real : 0.0;
@@ -449,7 +449,7 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
     a.padded = 1;
     ws = pw + copy_bytes(g.rows, g.k);
   }
-  const Plan plan = plan_tiles(g.m, g.rows, g.k, chunked<false, false>(a));
+  const Plan plan = plan_tiles(g.m, g.rows, g.k, chunked<false, false>(a, d->gated != 0));
   apply(plan, ws, a);
   rc = tile_forward(a, d->dtype, d->gated != 0, plan.tile, s);
   if (rc || plan.splits == 1) return rc;

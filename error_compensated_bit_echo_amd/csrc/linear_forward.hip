@@ -6,7 +6,7 @@ namespace echo {
 template <typename T, bool GATED>
 static int forward(const TileArgs& a, int tile, hipStream_t s) {
   constexpr int SI = GATED ? 4 : 2, SJ = GATED ? 1 : 2;  // a gated run is 64 rows of w, in one wavefront
-  if (chunked<false, false>(a)) {
+  if (chunked<false, false>(a, GATED)) {
     switch (tile) {
       case kTile256: return launch_tile<T, false, false, 256, 256, 4, 2, GATED, 2>(a, s);
       case kTile256x128: return launch_tile<T, false, false, 256, 128, 4, 2, GATED, 3>(a, s);

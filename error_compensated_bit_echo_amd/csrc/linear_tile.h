@@ -293,7 +293,9 @@ __global__ __launch_bounds__(64 * WI * WJ * WK, 2) void k_tile_dma(TileArgs a) {
   for (int i = 0; i < B::kPer; ++i) {
     const int q = i * NT + tid, r = q / B::kRow;
     cb[i] = B::place(r, q % B::kRow) * 8;
-    ob[i] = (int)((GATED ? (r >> 6) * 32 + (r & 31) : r) * a.ldb + cb[i]) * 2;
+    // gated, up rows lie J rows behind their gate's; a last tile's gate rows past J
+    // are up rows then, whose sums are not written
+    ob[i] = (int)(((GATED ? (r >> 6) * 32 + (r & 31) : r) + (GATED && (r >> 5 & 1) ? a.J : 0)) * a.ldb + cb[i]) * 2;
   }
   const T* pa = (const T*)a.a + (TA ? c0 * a.lda + i0 : i0 * a.lda + c0);
   const T* pb = (const T*)a.b + (TB ? c0 * a.ldb + j0 : j0 * a.ldb + c0);
@@ -324,15 +326,11 @@ __global__ __launch_bounds__(64 * WI * WJ * WK, 2) void k_tile_dma(TileArgs a) {
 #pragma unroll
       for (int i = 0; i < B::kPer; ++i) dma16(r, lb + (i * NT + wave * 64) * 8, ob[i]);
     } else {
-      const int64_t bytes = ((rows_b - 1) * a.ldb + whole) * 2;
-      const auto r = range_of(pb, bytes);
-      const auto up = range_of(GATED ? pb + a.J * a.ldb : pb, bytes);
+      const auto r = range_of(pb, ((rows_b - 1 + (GATED ? a.J : 0)) * a.ldb + whole) * 2);
 #pragma unroll
       for (int i = 0; i < B::kPer; ++i) {
         const int o = ob[i] + s * kC * 2;
-        // a wavefront's 64 chunks are eight rows, all of one half of a gated run
-        const bool is_up = GATED && ((i * NT + wave * 64) / B::kRow >> 5 & 1);
-        dma16(is_up ? up : r, lb + (i * NT + wave * 64) * 8, tail && cb[i] >= left ? kPast : o);
+        dma16(r, lb + (i * NT + wave * 64) * 8, tail && cb[i] >= left ? kPast : o);
       }
     }
   };
@@ -369,9 +367,8 @@ __global__ __launch_bounds__(64 * WI * WJ * WK, 2) void k_tile_dma(TileArgs a) {
         for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(fb[0][j], fa[0][i], acc[i][j], T{});
       return;
     }
-    if constexpr (GATED) load();
     read(0);
-    if constexpr (!GATED) load();
+    load();
     if constexpr (TA && TB) read(1);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
@@ -424,9 +421,10 @@ __global__ __launch_bounds__(64 * WI * WJ * WK, 2) void k_tile_dma(TileArgs a) {
 }
 
 // whether every 16-byte chunk of both operands is aligned and, along c, whole or
-// filled up with zeros
+// filled up with zeros, and within the loads' offsets
 template <bool TA, bool TB>
-bool chunked(const TileArgs& a) {
+bool chunked(const TileArgs& a, bool gated = false) {
+  if (gated && (2 * a.J + 256) * a.ldb * 2 >= INT64_C(0x7FFFFFF0)) return false;  // 31-bit offsets in w
   return aligned(a.a, 16) && aligned(a.b, 16) && a.lda % 8 == 0 && a.ldb % 8 == 0 &&
          ((TA && TB) || a.C % 8 == 0 || a.padded);
 }
