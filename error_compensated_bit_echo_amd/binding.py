@@ -491,12 +491,6 @@ def _rows_of(t, what):
     return (t.numel() // cols if cols else math.prod(shape[:-1])), cols
 
 
-def _same_pitch(a, b, what):
-    if a is not None and b is not None and a != b:
-        raise ValueError(f"{what}: the same row pitch is required (got {a} and {b})")
-    return a if a is not None else (b if b is not None else 0)
-
-
 def echo_norm(h, y, h_out, z, *, post="none", w_post=None, b_post=None, gate=None, scale=1.0,
               pre="rms", w_pre=None, b_pre=None, eps=1e-6, stats=None, stream=None) -> None:
     """h_out = h + scale * gate * N_post(y); z = N_pre(h_out), row by row.
@@ -510,15 +504,23 @@ def echo_norm(h, y, h_out, z, *, post="none", w_post=None, b_post=None, gate=Non
     dt, sdt = _dtype_of(h if y is None and z is None else z if y is None else y, "y, z"), h.dtype
     hp, ldh = _matrix(h, T, H, sdt, "h")
     yp, ldy = _matrix(y, T, H, dt, "y") if y is not None else (None, 0)
-    op, ldo = _matrix(h_out, T, H, sdt, "h_out") if h_out is not None else (None, None)
+    op, ldo = _matrix(h_out, T, H, sdt, "h_out") if h_out is not None else (None, ldh)
+    if ldo != ldh:
+        raise ValueError(f"h, h_out: the same row pitch is required (got {ldh} and {ldo})")
     G = 0 if gate is None else _rows_of(gate, "gate")[0]
-    d = EchoNormDescC(T, H, ldy, _same_pitch(ldh, ldo, "h, h_out"), G, DTYPES[dt], DTYPES[sdt],
-                      _code(NORMS, post, "post"), _code(NORMS, pre, "pre"), float(scale), float(eps))
-    _check(lib.echo_norm(C.byref(d), hp, yp, _dense(gate, (G, H), dt, "gate"),
-                         _dense(w_post, (H,), dt, "w_post"), _dense(b_post, (H,), dt, "b_post"),
-                         _dense(w_pre, (H,), dt, "w_pre"), _dense(b_pre, (H,), dt, "b_pre"), op,
-                         _dense(z, (T, H), dt, "z"), _dense(stats, (4, T), torch.float32, "stats"),
-                         _stream(stream)), "echo_norm")
+    d = EchoNormDescC(T, H, ldy, ldh, G, DTYPES[dt], DTYPES[sdt], NORMS.get(post, -1), NORMS.get(pre, -1), scale, eps)
+    if d.post < 0 or d.pre < 0:
+        _code(NORMS, post, "post"), _code(NORMS, pre, "pre")
+    # (absent vectors are not worth a call each: the smallest norms cost their host time)
+    rc = lib.echo_norm(C.byref(d), hp, yp, gate if gate is None else _dense(gate, (G, H), dt, "gate"),
+                       w_post if w_post is None else _dense(w_post, (H,), dt, "w_post"),
+                       b_post if b_post is None else _dense(b_post, (H,), dt, "b_post"),
+                       w_pre if w_pre is None else _dense(w_pre, (H,), dt, "w_pre"),
+                       b_pre if b_pre is None else _dense(b_pre, (H,), dt, "b_pre"), op,
+                       z if z is None else _dense(z, (T, H), dt, "z"),
+                       stats if stats is None else _dense(stats, (4, T), torch.float32, "stats"), _stream(stream))
+    if rc:
+        _check(rc, "echo_norm")
 
 
 def echo_norm_backward_workspace(tokens, hidden, gate_rows=0) -> int:

@@ -50,7 +50,7 @@ extern "C" {
 #define ECHO_ACT_SILU 4      /* p / (1 + exp(-p)) */
 
 #define ECHO_MAX_HIDDEN 16384             /* row length of the norms */
-#define ECHO_MAX_PITCH (INT64_C(1) << 21) /* row pitch (and k) of the products */
+#define ECHO_MAX_PITCH (INT64_C(1) << 21) /* any row pitch; k and the rows of w of the products */
 #define ECHO_MAX_ROWS (INT64_C(1) << 31)  /* tokens; m, n of the products */
 
 /* The norms around a block: u = N_post(y) on the block's output y, the

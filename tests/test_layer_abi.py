@@ -3,6 +3,8 @@ agree, and every bad argument is refused before anything is launched."""
 import ctypes as C
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -25,6 +27,42 @@ def test_library_exports_what_the_header_declares():
 def test_new_status_strings():
     for code in (-8, -9):
         assert B.status_string(code) != "unknown status"
+
+
+C_CONSUMER = r"""
+#include <stdio.h>
+#include "echo_layer.h"
+int main(void) {
+  echo_norm_desc n = {0};
+  echo_linear_desc l = {0};
+  if (echo_norm_backward_workspace(&n) != ECHO_ERR_SHAPE) return 1; /* hidden 0 */
+  n.tokens = 4; n.hidden = 8; n.gate_rows = 3;
+  if (echo_norm_backward_workspace(&n) != ECHO_ERR_SHAPE) return 2;
+  l.m = 4; l.n = 4; l.k = 4; l.dtype = ECHO_F32;
+  if (echo_linear_workspace(&l) != ECHO_ERR_TYPE) return 3;
+  l.dtype = ECHO_BF16; l.act = ECHO_ACT_SILU; l.gated = 1;
+  if (echo_linear_workspace(&l) < 0 || echo_linear_backward_workspace(&l) <= 0) return 4;
+  if (echo_linear(&l, 0, 0, 0, 0, 0, 0, 0, 0, 0) != ECHO_ERR_INVALID_ARGUMENT) return 5;
+  l.m = 0;
+  if (echo_linear(&l, 0, 0, 0, 0, 0, 0, 0, 0, 0) != ECHO_SUCCESS) return 6;
+  puts("ok");
+  return 0;
+}
+"""
+
+
+def test_header_is_plain_c(tmp_path):
+    """the header compiles as C11 and a program without Python links against it"""
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not available")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    (tmp_path / "c.c").write_text(C_CONSUMER)
+    exe = str(tmp_path / "c")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"),
+                    str(tmp_path / "c.c"), "-o", exe, B.LIB_PATH, "-L", os.path.join(rocm, "lib"), "-lamdhip64",
+                    f"-Wl,-rpath,{os.path.dirname(B.LIB_PATH)}:{os.path.join(rocm, 'lib')}"], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.returncode
 
 
 def desc(T=8, H=64, ld_y=0, ld_h=0, G=0, dt=0, sdt=0, post=0, pre=1, scale=1.0, eps=1e-6):
