@@ -115,54 +115,66 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   const int steps = (int)((c1 - c0 + kC - 1) / kC);
 
   // The thread's chunks of step 0.  Rows past an operand's end repeat its last
-  // row: what they add up to is not written.
+  // row: what they add up to is not written.  Across c a chunk that reaches past
+  // the operand's edge is read as the row's last eight elements, `ea` or `eb`
+  // places before its own, and moved when it is stored.
   const T *pa[A::kPer], *pb[B::kPer];
   int ca[A::kPer], cb[B::kPer];  // along c: the chunk's first element of the step; across: its row
+  int ea[A::kPer], eb[B::kPer];
 #pragma unroll
   for (int i = 0; i < A::kPer; ++i) {
     const int q = i * NT + tid, r = q / A::kRow, col = A::place(r, q % A::kRow) * 8;
     ca[i] = TA ? r : col;
-    pa[i] = (const T*)a.a + (TA ? (c0 + r) * a.lda + i0 + col : min(i0 + r, a.I - 1) * a.lda + c0 + col);
+    ea[i] = TA ? (int)max(i0 + col - (a.I - 8), (int64_t)0) : 0;
+    pa[i] = (const T*)a.a + (TA ? (c0 + r) * a.lda + i0 + col - ea[i] : min(i0 + r, a.I - 1) * a.lda + c0 + col);
   }
 #pragma unroll
   for (int i = 0; i < B::kPer; ++i) {
     const int q = i * NT + tid, r = q / B::kRow, col = B::place(r, q % B::kRow) * 8;
     cb[i] = TB ? r : col;
+    eb[i] = TB ? (int)max(j0 + col - (a.J - 8), (int64_t)0) : 0;
     if constexpr (TB) {
-      pb[i] = (const T*)a.b + (c0 + r) * a.ldb + j0 + col;
+      pb[i] = (const T*)a.b + (c0 + r) * a.ldb + j0 + col - eb[i];
     } else {
       const int64_t j = min(j0 + (GATED ? (r >> 6) * 32 + (r & 31) : r), a.J - 1);
       pb[i] = (const T*)a.b + (j + (GATED && (r >> 5 & 1) ? a.J : 0)) * a.ldb + c0 + col;
     }
   }
-  // every chunk of a whole step exists but for those across the operand's edge
-  const bool inner = (!TA || i0 + BI <= a.I) && (!TB || j0 + BJ <= a.J);
+  // whole steps of rows of a chunk or more are loaded without a guard
+  const bool wide = (!TA || a.I >= 8) && (!TB || a.J >= 8);
+  const bool edge = (TA && i0 + BI > a.I) || (TB && j0 + BJ > a.J);
+  auto whole = [&](int s) { return wide && c1 - c0 - (int64_t)s * kC >= kC; };
   u32x4 ra[D][A::kPer], rb[D][B::kPer];
   auto load = [&](u32x4 (&va)[A::kPer], u32x4 (&vb)[B::kPer], int s) {
     const int64_t c = (int64_t)s * kC, left = c1 - c0 - c;
-    if (left >= kC && inner) {
+    if (whole(s)) {
 #pragma unroll
       for (int i = 0; i < A::kPer; ++i) va[i] = *(const u32x4_a2*)(pa[i] + (TA ? c * a.lda : c));
 #pragma unroll
       for (int i = 0; i < B::kPer; ++i) vb[i] = *(const u32x4_a2*)(pb[i] + (TB ? c * a.ldb : c));
     } else if (left > 0) {
 #pragma unroll
-      for (int i = 0; i < A::kPer; ++i) {
-        const int col = A::place((i * NT + tid) / A::kRow, (i * NT + tid) % A::kRow) * 8;
-        va[i] = raw8(pa[i] + (TA ? c * a.lda : c), TA ? (ca[i] < left ? a.I - (i0 + col) : 0) : left - ca[i]);
-      }
+      for (int i = 0; i < A::kPer; ++i)
+        va[i] = raw8(pa[i] + ea[i] + (TA ? c * a.lda : c), TA ? (ca[i] < left ? 8 - ea[i] : 0) : left - ca[i]);
 #pragma unroll
-      for (int i = 0; i < B::kPer; ++i) {
-        const int col = B::place((i * NT + tid) / B::kRow, (i * NT + tid) % B::kRow) * 8;
-        vb[i] = raw8(pb[i] + (TB ? c * a.ldb : c), TB ? (cb[i] < left ? a.J - (j0 + col) : 0) : left - cb[i]);
-      }
+      for (int i = 0; i < B::kPer; ++i)
+        vb[i] = raw8(pb[i] + eb[i] + (TB ? c * a.ldb : c), TB ? (cb[i] < left ? 8 - eb[i] : 0) : left - cb[i]);
     }
   };
   auto stage = [&](const u32x4 (&va)[A::kPer], const u32x4 (&vb)[B::kPer], int s) {
+    const bool move = edge && whole(s);
+    auto put = [&](int place, u32x4 w, int by) {
+      if (move) {  // (a chunk wholly past the edge holds anything)
+        Raw<T> r = {w};
+        MoveDown{by}(r);
+        w = r.w;
+      }
+      *(u32x4*)(lds[s & 1] + place) = w;
+    };
 #pragma unroll
-    for (int i = 0; i < A::kPer; ++i) *(u32x4*)(lds[s & 1] + (i * NT + tid) * 8) = va[i];
+    for (int i = 0; i < A::kPer; ++i) put((i * NT + tid) * 8, va[i], ea[i]);
 #pragma unroll
-    for (int i = 0; i < B::kPer; ++i) *(u32x4*)(lds[s & 1] + BI * kC + (i * NT + tid) * 8) = vb[i];
+    for (int i = 0; i < B::kPer; ++i) put(BI * kC + (i * NT + tid) * 8, vb[i], eb[i]);
   };
 
   f32x4 acc[TI][TJ];
