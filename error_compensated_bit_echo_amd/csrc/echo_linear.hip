@@ -29,8 +29,10 @@ struct SlopeArgs {
   int32_t act, gated, wide;  // wide: 8, 16 or 32
 };
 
-// WHOLE: rows are whole vectors, so that two rows' loads are on their way at once
-// without a branch at whose end they would be waited for.
+// Two rows' loads are on their way at once, without a branch at whose end they
+// would be waited for.  WHOLE: rows are whole vectors.  Otherwise a row's last
+// vector is read as the row's last eight elements and moved down, and rows
+// under a vector are read element by element.
 template <typename T, bool GATED, bool WHOLE>
 __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
   __shared__ float lds[GATED ? 2 : 1][256 * 8 + 32 * 8];
@@ -69,20 +71,26 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
       if (GATED) su[e] += p[e];
     }
   };
-  if (WHOLE && n > 0) {
+  const int back = !WHOLE && n < 8 ? 8 - n : 0;
+  if ((WHOLE || a.n >= 8) && n > 0) {
     for (int64_t r = r0 + ty; r < r1; r += 2 * high) {
       Raw<T> d[2], p[2], u[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // past the end the last row once more
         const int64_t at = min(r + k * high, r1 - 1);
-        d[k] = fetch_at<true>((const T*)a.dout + at * a.ld_out + col);
-        if (a.p) p[k] = fetch_at<true>((const T*)a.p + at * cols + col);
-        if (GATED && a.p) u[k] = fetch_at<true>((const T*)a.p + at * cols + a.n + col);
+        d[k] = fetch_at<true>((const T*)a.dout + at * a.ld_out + col - back);
+        if (a.p) p[k] = fetch_at<true>((const T*)a.p + at * cols + col - back);
+        if (GATED && a.p) u[k] = fetch_at<true>((const T*)a.p + at * cols + a.n + col - back);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (r + k * high >= r1) continue;
         float fd[8], fp[8], fu[8];
+        if constexpr (!WHOLE) {
+          MoveDown{back}(d[k]);
+          if (a.p) MoveDown{back}(p[k]);
+          if (GATED && a.p) MoveDown{back}(u[k]);
+        }
         unpack_raw(d[k], fd);
         if (a.p) unpack_raw(p[k], fp);
         if (GATED && a.p) unpack_raw(u[k], fu);
