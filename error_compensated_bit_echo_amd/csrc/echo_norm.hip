@@ -321,12 +321,20 @@ __device__ __forceinline__ void flush(float (&acc)[ITEMS][8], const int (&col)[I
 
 // FULL: with a post norm or a gate; else dy = scale dh and only the pre
 // norm's parameters have gradients.  BIAS: with a bias's gradient.  Without them
-// there are fewer accumulators, so more rows in flight.  A workgroup walks `chunk` consecutive rows and keeps the sums over
-// them in registers, so the row data is read once for all outputs.
+// there are fewer accumulators, so more rows in flight.  A workgroup walks
+// `chunk` consecutive rows and keeps the sums over them, so the row data is read
+// once for all outputs.  The sums stand in registers; but more than eight
+// wavefronts have 128 registers a lane, so dw1's, dg's and, where it fits, db1's
+// stand in LDS there (4072 x 4100 f16 with all five sums: 143 us against 242
+// with all in registers, which spill, and 175 with db2's in LDS as well; 4072 x
+// 8200: 600 against 673.  Up to eight wavefronts gain nothing by it.)
 template <typename T, typename S, int WAVES, int ITEMS, bool FULL, bool BIAS, RowEnd END>
 __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1 ? 3 : 1) void k_norm_backward(
     NormBackArgs a) {
   constexpr bool MANY = WAVES > 1;
+  constexpr bool IN_LDS = FULL && WAVES == kMostWaves;
+  constexpr int kFar = BIAS && ITEMS == 1 ? 3 : 2;
+  __shared__ f32x4 far[IN_LDS ? kFar * ITEMS * 2 : 1][IN_LDS ? threads_of(WAVES) : 1];
   constexpr int kRows = MANY ? 1 : kSideBySide;
   __shared__ float slots[MANY ? 2 * 4 * kMostWaves : 1];
   __shared__ float comb[MANY ? 1 : kSideBySide * 512 * ITEMS];
@@ -360,6 +368,25 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
   zero(dw1);
   zero(db1);
   zero(dg);
+  // dw1, dg and db1 stand in registers or in the thread's own place in LDS
+  enum { kFarW, kFarGate, kFarB };
+  auto far_read = [&](int k, int i, float (&v)[8]) {
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = far[(k * ITEMS + i) * 2 + e / 4][threadIdx.x][e % 4];
+    }
+  };
+  auto far_write = [&](int k, int i, const float (&v)[8]) {
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        far[(k * ITEMS + i) * 2 + q][threadIdx.x] = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kFar; ++k)
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) far_write(k, i, dw2[i]);  // zeros
   int64_t s1;
   for (int64_t s0 = r0; s0 < r1; s0 = s1) {
     s1 = FULL && a.gate_sum == kGateWhole ? min(s0 + (int64_t)a.rows_per_gate, r1) : r1;
@@ -483,8 +510,10 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
                 for (int e = 0; e < 8; ++e) u[e] *= d[i][e];
                 at[i].template store<true>((T*)a.dgate + row * H + col[i], u);
               } else {
+                far_read(kFarGate, i, dg[i]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dg[i][e] = fmaf(u[e], d[i][e], dg[i][e]);
+                far_write(kFarGate, i, dg[i]);
               }
             }
             at[i].unpack(gate.raw[i], b);
@@ -492,10 +521,17 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
             for (int e = 0; e < 8; ++e) d[i][e] *= b[e];
           }
           if (a.post != ECHO_NORM_NONE) {
+            far_read(kFarW, i, dw1[i]);
+            if constexpr (kFar == 3) far_read(kFarB, i, db1[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               dw1[i][e] = fmaf(d[i][e], y[i][e], dw1[i][e]);
               if constexpr (BIAS) db1[i][e] += d[i][e];
+            }
+            far_write(kFarW, i, dw1[i]);
+            if constexpr (kFar == 3) far_write(kFarB, i, db1[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
               if (a.w_post) d[i][e] *= w[e];
               sh = fmaf(d[i][e], y[i][e], sh);
               sg += d[i][e];
@@ -525,8 +561,12 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
     }
     if constexpr (FULL) {
       if (a.gate_sum == kGateWhole) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) far_read(kFarGate, i, dg[i]);
         flush<T, MANY, ITEMS>(dg, col, (T*)a.dgate + s0 / a.rows_per_gate * H, H, comb);
         zero(dg);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) far_write(kFarGate, i, dg[i]);
       }
     }
   }
@@ -536,6 +576,12 @@ __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1
   if constexpr (BIAS)
     if (a.want >> kDbPre & 1) flush<float, MANY, ITEMS>(db2, col, p + kDbPre * plane, H, comb);
   if constexpr (FULL) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      far_read(kFarW, i, dw1[i]);
+      far_read(kFarGate, i, dg[i]);
+      if constexpr (kFar == 3) far_read(kFarB, i, db1[i]);
+    }
     if (a.want >> kDwPost & 1) flush<float, MANY, ITEMS>(dw1, col, p + kDwPost * plane, H, comb);
     if constexpr (BIAS)
       if (a.want >> kDbPost & 1) flush<float, MANY, ITEMS>(db1, col, p + kDbPost * plane, H, comb);
@@ -633,7 +679,7 @@ int check_desc(const echo_norm_desc* d, Geometry& g) {
 
 // Wavefronts of a row and vectors of a thread.  Short rows take one wavefront and
 // need no barrier; longer ones as many as hold them.  The forward pass holds two
-// vectors a thread past 2048 elements (8192 x 4096: 48.5 us against 51.7 with one,
+// vectors a thread past 2048 elements (8192 x 4096: 45.6 us against 51.7 with one,
 // which has twice the wavefronts to wait for at a barrier); the backward pass,
 // whose accumulators fill the registers, one.
 struct RowShape {

@@ -6,7 +6,7 @@
 //   dx        dx  = dp w      A = dp [m][n]    B = w [n][k]^T  c across B's rows
 //   dw        dw  = dp^T x    A = dp [m][n]^T  B = x [m][k]^T  c across both
 // A workgroup computes a BI x BJ tile of C in steps of kC = 64 along c.  Both
-// operands' tiles are staged in LDS, two stages deep, and feed
+// operands' tiles are staged in LDS, two to four stages deep, and feed
 // v_mfma_f32_16x16x32: lane l of a wavefront holds, for row (or column) l % 16
 // of an operand's 16, the eight elements c = 8 (l / 16) .. + 7 of the 32.
 // B's fragment goes into the instruction's first operand, so a lane's four sums
