@@ -148,6 +148,17 @@ def test_many_rows(T, H, groups):
     check_backward(c, "rms", "rms", h_out, stats)
 
 
+@pytest.mark.parametrize("T,H,groups", [(1030, 4100, 515), (600, 8200, 300), (520, 4104, 2), (770, 8195, 1)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_many_long_rows(T, H, groups, kind):
+    """several rows to a workgroup of more than eight wavefronts, whose sums over
+    the rows stand in LDS; with biases' gradients (layer) and without"""
+    print(f"norm T={T} H={H} groups={groups} {kind}", flush=True)
+    c = case(T, H, torch.float16, torch.float32, kind, kind, groups, seed=5)
+    h_out, stats = check_forward(c, kind, kind)
+    check_backward(c, kind, kind, h_out, stats)
+
+
 def test_mean_far_from_zero_costs_no_digits():
     c = case(8, 1000, torch.float32, torch.float32, "none", "layer", 0, mean=300.0)
     check_forward(c, "none", "layer")
