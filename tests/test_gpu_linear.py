@@ -115,6 +115,17 @@ def test_activations(act, gated):
         backward(c, act, gated, p)
 
 
+@pytest.mark.parametrize("m,n,k", [(2600, 1003, 40), (1300, 5, 41), (900, 9, 1001), (700, 78, 5)])
+def test_many_odd_rows(m, n, k):
+    """rows that end inside a vector, and rows under one, in runs of several rows
+    and in whole steps along the contraction"""
+    for gated, act in ((False, "none"), (False, "gelu"), (True, "silu")):
+        print(f"linear m={m} n={n} k={k} {act} gated={gated}", flush=True)
+        c = case(m, n, k, torch.float16, gated, seed=13)
+        _, p = forward(c, act, gated)
+        backward(c, act, gated, p)
+
+
 @pytest.mark.parametrize("m,n,k", [(1025, 2056, 136), (2050, 1032, 72), (4100, 520, 80), (70, 8200, 64),
                                    (6000, 136, 4104), (513, 100, 9000)])
 def test_many_tiles(m, n, k):
