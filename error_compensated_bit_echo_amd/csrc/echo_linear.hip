@@ -20,6 +20,13 @@ namespace {
 // its columns in binary32 for the bias.  A thread holds 8 columns and walks
 // down the rows of its workgroup's run; `wide` threads lie side by side, 256 /
 // wide above each other.  Bound by HBM: 2 bytes in per dout and p element, 2 out.
+// The products read dp in 16 bits because the matrix cores do; the sums and the
+// bias's gradient stay in binary32.  That is the rounding a caller who keeps dp as a
+// tensor has too.  dp in two 16-bit parts, its rounding and the rest, would leave
+// dx and dw the one rounding of their own, at twice the products: 32768 x 768 x
+// 1024 bf16, root-mean-square error of dx and dw 0.0023 -> 0.0017 for 67 + 75 us ->
+// 104 + 116; 8192 x 1792 x 4096 f16, 0.00029 -> 0.00021 for 120 + 129 us -> 199 +
+// 209.  Half's range is the caller's to mind, by the scale of dout (echo_layer.h).
 struct SlopeArgs {
   const void *dout;
   const void* p;  // nullable: no activation, dp is a copy of dout

@@ -19,7 +19,12 @@
  *   - Sums, statistics and everything between reading an input and writing an
  *     output are binary32; each output is rounded once, to nearest even.
  *     One exception: the products of echo_linear_backward read the gradient of
- *     the pre-activation rounded to `dtype`, the matrix cores' operand type.
+ *     the pre-activation, dp, rounded to `dtype`, the matrix cores' operand type:
+ *     one more rounding in every term of dx and dw (not of dbias).  In half
+ *     precision its range counts too: a dp past 65504 is infinite, one below
+ *     2^-14 keeps fewer digits.  dx, dw and dbias are linear in dout, so a
+ *     caller's power-of-two scale on dout moves dp within the range, as it does
+ *     for dx and dw themselves.
  *   - No atomics: the same inputs give the same bits on every call.
  *   - inf and NaN go through as the formulas have them: a row that holds one
  *     spoils that row of the norms and nothing else, an operand of a product
