@@ -92,7 +92,8 @@ __device__ __forceinline__ void act_slope(float p, float& v, float& d) {
   } else if constexpr (ACT == ECHO_ACT_GELU_TANH) {
     const float s = gelu_tanh_gate(p);
     v = p * s;
-    d = fmaf(v * (1.f - s), 1.59576912f * fmaf(0.134145f, p * p, 1.f), s);
+    // p^2 capped where 1 - s or v is 0 long before it, so that it is never infinite
+    d = fmaf(v * (1.f - s), 1.59576912f * fmaf(0.134145f, fminf(p * p, 1e30f), 1.f), s);
   } else if constexpr (ACT == ECHO_ACT_SILU) {
     const float s = sigmoid(p);
     v = p * s;
