@@ -245,6 +245,7 @@ int check_desc(const echo_linear_desc* d, Geometry& g) {
   g.n = d->n;
   g.k = d->k;
   g.rows = d->gated ? 2 * d->n : d->n;
+  if (g.m * g.k > ECHO_MAX_PRODUCT || g.m * g.rows > ECHO_MAX_PRODUCT) return ECHO_ERR_SHAPE;
   if (pitch(d->ld_x, g.k, g.ld_x) || pitch(d->ld_w, g.k, g.ld_w) || pitch(d->ld_out, g.n, g.ld_out) ||
       pitch(d->ld_r, g.n, g.ld_r))
     return ECHO_ERR_SHAPE;
@@ -252,47 +253,6 @@ int check_desc(const echo_linear_desc* d, Geometry& g) {
 }
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-// Which tile, and into how many splits of the contraction.  The estimate of a
-// choice: a compute unit works through n tiles, each at `step` us a step and
-// `over` us from its last step to the next tile's first, and a tile takes at
-// least `alone` us a step, when it has no other to overlap with (as measured,
-// bf16); splits cost writing and reading their binary32 sums and one more
-// launch.  It is the rule; nothing is tuned to a shape.
-struct TileCost { int bi, bj; float step, over, alone; };
-constexpr TileCost kChunkedCost[kTileKinds] = {{256, 256, 1.45f, 8.5f, 1.45f},
-                                               {256, 128, 0.88f, 4.5f, 0.88f},
-                                               {128, 128, 0.45f, 1.8f, 0.62f},
-                                               {64, 64, 0.185f, 0.8f, 0.22f}};
-constexpr TileCost kStagedCost[kTileKinds] = {
-    {0, 0, 0, 0, 0}, {0, 0, 0, 0, 0}, {128, 128, 1.00f, 2.0f, 1.10f}, {64, 64, 0.38f, 1.0f, 0.50f}};
-constexpr int64_t kMostPart = INT64_C(256) << 20;  // bytes of partial sums
-
-struct Plan { int tile; int64_t splits, chunk, part_bytes; double us; };
-
-Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
-  const int64_t steps = (C + kC - 1) / kC;
-  Plan best = {kTile64, 1, steps * kC, 0, 1e30};
-  for (int t = 0; t < kTileKinds; ++t) {
-    const TileCost& k = is_chunked ? kChunkedCost[t] : kStagedCost[t];
-    if (k.bi == 0) continue;
-    const int64_t tiles = ((I + k.bi - 1) / k.bi) * ((cols + k.bj - 1) / k.bj);
-    // at least four steps to a split, and no more than four rounds of workgroups
-    const int64_t room = tiles > 0 ? 1024 / tiles : 1, deep = steps / 4;
-    const int64_t most = room < deep ? (room < 32 ? room : 32) : (deep < 32 ? deep : 32);
-    for (int64_t splits = 1; splits <= most || splits == 1; splits += splits < 16 ? 1 : 4) {
-      const int64_t each = (steps + splits - 1) / splits;
-      const int64_t real = each > 0 ? (steps + each - 1) / each : 1;  // splits that have steps
-      const double bytes = real > 1 ? 4.0 * (double)I * (double)cols * (double)real : 0.0;
-      if (bytes > (double)kMostPart) break;
-      const double per_cu = (double)((tiles * real + 255) / 256);
-      const double shared = per_cu * ((double)each * k.step + k.over), lone = (double)each * k.alone + k.over;
-      const double us = (shared > lone ? shared : lone) + (real > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
-      if (us < best.us) best = {t, real > 0 ? real : 1, each * kC, real > 1 ? (int64_t)bytes : 0, us};
-    }
-  }
-  return best;
-}
 
 // partial sums of either kind of operands fit
 int64_t part_bytes(int64_t I, int64_t cols, int64_t C) {

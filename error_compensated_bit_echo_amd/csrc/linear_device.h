@@ -27,6 +27,7 @@
 
 #include "echo_layer.h"
 #include "layer_device.h"
+#include "linear_plan.h"
 
 namespace echo {
 
@@ -35,8 +36,6 @@ namespace echo {
 typedef __attribute__((address_space(3))) short lds_short;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kC = 64;  // contraction length of a step
 
 struct TileArgs {
   const void *a, *b;
@@ -47,7 +46,7 @@ struct TileArgs {
   void *out, *p;
   const void *bias, *residual;
   int64_t ldo, ldr;
-  uint32_t tiles_i, tiles_j, splits;
+  uint32_t tiles_i, tiles_j, splits, workgroups;  // workgroups: tiles of all splits
   int32_t act;
   int32_t padded;   // rows along c are followed by zeros up to a whole chunk
 };

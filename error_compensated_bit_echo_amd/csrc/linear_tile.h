@@ -108,8 +108,10 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+  const uint32_t b = blockIdx.y * gridDim.x + blockIdx.x;
+  if (b >= a.workgroups) return;
   uint32_t ti, tj, split;
-  tile_of(blockIdx.x, gridDim.x, a.tiles_i, a.tiles_j, ti, tj, split);
+  tile_of(b, a.workgroups, a.tiles_i, a.tiles_j, ti, tj, split);
   const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * OUT;
   const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
   const int steps = (int)((c1 - c0 + kC - 1) / kC);
@@ -283,8 +285,10 @@ __global__ __launch_bounds__(64 * WI * WJ * WK, 2) void k_tile_dma(TileArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int own = wave % (WI * WJ), half = wave / (WI * WJ);  // half: 0 where WK is 1
   const int wi = own % WI * (BI / WI), wj = own / WI * (BJ / WJ);
+  const uint32_t b = blockIdx.y * gridDim.x + blockIdx.x;
+  if (b >= a.workgroups) return;
   uint32_t ti, tj, split;
-  tile_of(blockIdx.x, gridDim.x, a.tiles_i, a.tiles_j, ti, tj, split);
+  tile_of(b, a.workgroups, a.tiles_i, a.tiles_j, ti, tj, split);
   const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * OUT;
   const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
   const int steps = (int)((c1 - c0 + kC - 1) / kC);
@@ -448,19 +452,16 @@ int launch_tile(TileArgs a, hipStream_t s) {
   const int64_t ti = (a.I + BI - 1) / BI, tj = (a.J + out - 1) / out;
   constexpr int NT = 64 * WI * WJ * WK;
   if (ti * tj == 0) return ECHO_SUCCESS;
-  if (ti * tj > (int64_t)(0xFFFFFFFFu / NT) / a.splits) return ECHO_ERR_SHAPE;
   a.tiles_i = (uint32_t)ti;
   a.tiles_j = (uint32_t)tj;
-  const dim3 grid(a.tiles_i * a.tiles_j * a.splits);
+  a.workgroups = a.tiles_i * a.tiles_j * a.splits;  // below 2^32 by ECHO_MAX_PRODUCT
+  const TileGrid g = grid_of(a.workgroups, NT);
+  const dim3 grid(g.x, g.y);
   if constexpr (S > 0) return launch(k_tile_dma<T, TA, TB, BI, BJ, WI, WJ, GATED, S, WK>, grid, dim3(NT), s, a);
   else return launch(k_tile<T, TA, TB, BI, BJ, WI, WJ, GATED, -S>, grid, dim3(NT), s, a);
 }
 
 }  // namespace
-
-// Tiles, largest first; operands that are not chunked take kTile128 or kTile64
-// through registers.
-enum TileKind { kTile256 = 0, kTile256x128 = 1, kTile128 = 2, kTile64 = 3, kTileKinds = 4 };
 
 // The products, one source file each.
 int tile_forward(const TileArgs& a, int32_t dtype, bool gated, int tile, hipStream_t s);

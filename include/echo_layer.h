@@ -56,7 +56,8 @@ extern "C" {
 
 #define ECHO_MAX_HIDDEN 16384             /* row length of the norms */
 #define ECHO_MAX_PITCH (INT64_C(1) << 21) /* any row pitch; k and the rows of w of the products */
-#define ECHO_MAX_ROWS (INT64_C(1) << 31)  /* tokens; m, n of the products */
+#define ECHO_MAX_ROWS (INT64_C(1) << 31)  /* tokens; m of the products */
+#define ECHO_MAX_PRODUCT (INT64_C(1) << 42) /* m times k, m times the rows of w */
 
 /* The norms around a block: u = N_post(y) on the block's output y, the
  * residual update h' = h + scale * gate (.) u, and z = N_pre(h') for the next
@@ -117,7 +118,9 @@ int echo_norm_backward(const echo_norm_desc* d, const void* dz, const void* dh_o
  * Gated, w has 2n rows, the gate's first and the up rows behind them; bias,
  * p, and the gradients of w and bias have the same order. */
 typedef struct echo_linear_desc {
-  int64_t m, n, k;   /* each may be 0; m <= ECHO_MAX_ROWS, k and the rows of w <= ECHO_MAX_PITCH */
+  int64_t m, n, k;   /* each may be 0; m <= ECHO_MAX_ROWS, k and the rows of w <= ECHO_MAX_PITCH,
+                        m k and m times the rows of w <= ECHO_MAX_PRODUCT (8 TiB, more than
+                        a device holds) */
   int64_t ld_x;      /* row pitch of x */
   int64_t ld_w;      /* row pitch of w */
   int64_t ld_out;    /* row pitch of out, and of its gradient */
