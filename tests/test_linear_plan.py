@@ -8,6 +8,7 @@ import subprocess
 import pytest
 
 from error_compensated_bit_echo_amd import binding as B
+from linear_tile_cases import CASES, TILES, product_of
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -44,3 +45,18 @@ def test_long_products_have_a_workspace_answer():
     for m in ((1 << 29) - 1, 1 << 29, 600_000_000, 1 << 30, 1 << 31):
         for n, k in ((1, 1), (8, 8), (8, 64), (64, 7), (128, 8)):
             assert B.echo_linear_workspace(m, n, k) >= 0 and B.echo_linear_backward_workspace(m, n, k) >= 0
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_shapes_of_the_tile_tests_take_their_tiles(plan, name):
+    """tests/test_gpu_linear_tiles.py runs the large tiles as long as this holds"""
+    case = CASES[name]
+    r = subprocess.run([plan, "choose", *map(str, product_of(case)), "1"], capture_output=True, text=True, check=True)
+    tile, splits = map(int, r.stdout.split())
+    assert tile == TILES[case[6]] and (splits > 1) == case[7], (tile, splits)
+
+
+def test_odd_rows_of_the_tile_tests_are_copied():
+    """the forward case of odd rows reaches its tile through copies with whole rows"""
+    m, n, k, act, gated = CASES["out 256 copied rows"][:5]
+    assert B.echo_linear_workspace(m, n, k, act=act, gated=gated) >= 2 * (m + n) * ((k + 7) // 8 * 8)
