@@ -86,3 +86,54 @@ def backward(dout, x, w, p, kind, gated):
     else:
         dp = d if kind == "none" else d * act(p.double(), kind)[1]
     return {"dx": dp @ w, "dw": dp.T.contiguous() @ x, "dbias": dp.sum(0)}
+
+
+def _norm_back(d, da, v, kind, w, mean, rstd):
+    """gradient of v for the gradient d of N(v), with magnitudes; the normalized row
+    with its own"""
+    if kind == "none":
+        return d, da, v, v.abs()
+    hat = (v - mean[:, None]) * rstd[:, None]
+    hata = (v.abs() + mean.abs()[:, None]) * rstd[:, None]
+    g, ga = (d, da) if w is None else (d * w, da * w.abs())
+    s, sa = g - hat * (g * hat).mean(1, keepdim=True), ga + hata * (ga * hata).mean(1, keepdim=True)
+    if kind == "layer":
+        s, sa = s - g.mean(1, keepdim=True), sa + ga.mean(1, keepdim=True)
+    return s * rstd[:, None], sa * rstd[:, None], hat, hata
+
+
+def norm_backward(dz, dh_out, h_out, y, stats, post, w_post, b_post, gate, scale, pre, w_pre):
+    """{name: (exact, magnitude)} of echo_norm_backward's outputs, binary64, where the
+    tensors are"""
+    dz, dh_out, h_out, y, st, w_post, b_post, w_pre, g = (
+        None if t is None else t.double() for t in (dz, dh_out, h_out, y, stats, w_post, b_post, w_pre, gate))
+    T, H = next(t for t in (dz, dh_out, y) if t is not None).shape
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    dh = torch.zeros_like(dz) if dh_out is None else dh_out
+    dha, out = dh.abs(), {}
+    if pre != "none":
+        back, ba, hat, hata = _norm_back(dz, dz.abs(), h_out, pre, w_pre, st[2], st[3])
+        dh, dha = dh + back, dha + ba
+        out["dw_pre"] = ((dz * hat).sum(0), (dz.abs() * hata).sum(0))
+        out["db_pre"] = (dz.sum(0), dz.abs().sum(0))
+    out["dh"] = (dh, dha)
+    du, dua = scale * dh, abs(scale) * dha
+    if g is not None:
+        G = g.shape[0]
+        if y is not None:
+            u, ua = y, y.abs()
+            if post != "none":
+                u, ua = (y - st[0][:, None]) * st[1][:, None], (y.abs() + st[0].abs()[:, None]) * st[1][:, None]
+                u, ua = (u, ua) if w_post is None else (u * w_post, ua * w_post.abs())
+                u, ua = (u, ua) if b_post is None else (u + b_post, ua + b_post.abs())
+            out["dgate"] = ((du * u).view(G, -1, H).sum(1), (dua * ua).view(G, -1, H).sum(1))
+        of_row = torch.arange(T, device=g.device) // (T // G)
+        du, dua = du * g[of_row], dua * g[of_row].abs()
+    if post == "none":
+        out["dy"] = (du, dua)
+        return out
+    dy, dya, hat, hata = _norm_back(du, dua, y, post, w_post, st[0], st[1])
+    out["dy"] = (dy, dya)
+    out["dw_post"] = ((du * hat).sum(0), (dua * hata).sum(0))
+    out["db_post"] = (du.sum(0), dua.sum(0))
+    return out

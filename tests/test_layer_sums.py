@@ -42,3 +42,24 @@ def test_the_formulas_are_those_of_the_reference(kind, gated):
     a, b = S.backward(dout, x, w, p, kind, gated), R.linear_backward(dout, x, w, p, kind, gated)
     for name in ("dx", "dw", "dbias"):
         assert torch.allclose(a[name], torch.from_numpy(b[name][0]), rtol=1e-12, atol=1e-12), name
+
+
+@pytest.mark.parametrize("groups", [0, 1, 4])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+def test_the_norms_formulas_are_those_of_the_reference(post, pre, groups):
+    gen = torch.Generator().manual_seed(6)
+    T, H = 8, 11
+    rand = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)  # noqa: E731
+    vec = lambda kind: (rand(H), rand(H) if kind == "layer" else None) if kind != "none" else (None, None)  # noqa: E731
+    h, y, dz, dh_out = rand(T, H), rand(T, H) + 0.3, rand(T, H), rand(T, H)
+    (w1, b1), (w2, b2) = vec(post), vec(pre)
+    gate = rand(groups, H) if groups else None
+    f = R.norm_forward(h, y, post, w1, b1, gate, 0.75, pre, w2, b2, 1e-5)
+    h_out, stats = torch.from_numpy(f["h_out"][0]), torch.from_numpy(f["stats"][0])
+    args = (dz if pre != "none" else None, dh_out, h_out, y, stats, post, w1, b1, gate, 0.75, pre, w2)
+    a, b = S.norm_backward(*args), R.norm_backward(*args)
+    assert set(a) == set(b)
+    for name in a:
+        assert torch.allclose(a[name][0], torch.from_numpy(b[name][0]), rtol=1e-11, atol=1e-12), name
+        assert (a[name][1] <= torch.from_numpy(b[name][1]) * (1 + 1e-9)).all(), name
