@@ -325,9 +325,11 @@ __device__ __forceinline__ void flush(float (&acc)[ITEMS][8], const int (&col)[I
 // `chunk` consecutive rows and keeps the sums over them, so the row data is read
 // once for all outputs.  The sums stand in registers; but more than eight
 // wavefronts have 128 registers a lane, so dw1's, dg's and, where it fits, db1's
-// stand in LDS there (4072 x 4100 f16 with all five sums: 143 us against 242
-// with all in registers, which spill, and 175 with db2's in LDS as well; 4072 x
-// 8200: 600 against 673.  Up to eight wavefronts gain nothing by it.)
+// stand in LDS there (4072 x 4100 f16 with all five sums, the same inputs each
+// time: 143 us against 242 with all in registers, which spill, and 175 with db2's
+// in LDS as well; 4072 x 8200: 600 against 673.  Up to eight wavefronts gain
+// nothing by it.)  Sixteen wavefronts with two vectors a lane spill all the same,
+// 103 registers and more: rows past 8192 take 4 times their floor and more.
 template <typename T, typename S, int WAVES, int ITEMS, bool FULL, bool BIAS, RowEnd END>
 __global__ __launch_bounds__(threads_of(WAVES), FULL && WAVES <= 8 && ITEMS == 1 ? 3 : 1) void k_norm_backward(
     NormBackArgs a) {
@@ -681,7 +683,9 @@ int check_desc(const echo_norm_desc* d, Geometry& g) {
 // need no barrier; longer ones as many as hold them.  The forward pass holds two
 // vectors a thread past 2048 elements (8192 x 4096: 45.6 us against 51.7 with one,
 // which has twice the wavefronts to wait for at a barrier); the backward pass,
-// whose accumulators fill the registers, one.
+// whose accumulators fill the registers, one (without a post norm and a gate two to
+// 1024, so that such rows need no barrier; and two past 8192, where a workgroup
+// has no more wavefronts).
 struct RowShape {
   int waves, items, threads;  // waves: the kernel's WAVES
   int64_t rows;               // of a workgroup at a time

@@ -142,7 +142,8 @@ int echo_linear(const echo_linear_desc* d, const void* x, const void* w, const v
                 const void* residual, void* out, void* p, void* workspace,
                 int64_t workspace_bytes, echo_stream_t stream);
 
-/* Bytes of workspace echo_linear_backward needs, or a negative ECHO_ERR_*. */
+/* Bytes of workspace echo_linear_backward needs, whichever of its outputs are
+ * asked for, or a negative ECHO_ERR_*. */
 int64_t echo_linear_backward_workspace(const echo_linear_desc* d);
 
 /* Gradients of echo_linear from dout (pitch ld_out) and the forward call's x,

@@ -110,8 +110,8 @@ def check_backward(c, post, pre, h_out, stats, scale=0.75, in_place=False):
 
 
 TYPE_PAIRS = [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32"), ("f32", "f32")]
-# around the row shapes: one wavefront (to 512, to 1024), four (to 2048, to
-# 4096), sixteen (to 8192, to 16384); lengths that are no multiple of 8
+# around the row shapes: one wavefront (to 512, to 1024), up to eight (to 4096),
+# up to sixteen (to 8192, to 16384); lengths that are no multiple of 8
 LENGTHS = [(1, 1), (3, 7), (5, 64), (9, 511), (6, 512), (7, 513), (5, 1024), (3, 1025), (3, 2048), (2, 2051),
            (1, 4096), (2, 4097), (2, 8192), (2, 8195), (1, 16384), (3, 16381)]
 
