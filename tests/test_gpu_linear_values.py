@@ -54,3 +54,28 @@ def test_slopes_at_the_far_ends(dt, act, gated):
     assert np.isfinite(exact).all()
     for r in range(m):
         R.close(dx[r], exact, magnitude, UNITS, f"row {r}")
+
+
+def test_halfs_range_of_dp_follows_the_scale_of_dout():
+    """dp is rounded to half: past its largest value infinite, under its normals short of
+    digits, both moved into the range by a power of two on dout"""
+    n = 16
+    up = torch.tensor([2.0 ** 14, 2.0 ** 13, 2.0 ** -10, 2.0 ** -11] * (n // 4), dtype=torch.float16)
+    odd = 1.0 + 2.0 ** -10  # the smallest half above 1
+    kept = torch.cat([torch.ones(n, dtype=torch.float16), up])[None].contiguous()
+    w = torch.cat([torch.eye(n), torch.zeros(n, n)]).to(torch.float16)
+    ws = torch.empty(B.echo_linear_backward_workspace(1, n, n, gated=True), dtype=torch.uint8, device=DEV)
+
+    def dx(scale):
+        dout, got = torch.full((1, n), odd * scale, dtype=torch.float16), torch.empty(1, n, dtype=torch.float16, device=DEV)
+        B.echo_linear_backward(on(dout), torch.zeros(1, n, dtype=torch.float16, device=DEV), on(w), on(kept), got, None,
+                               gated=True, workspace=ws)
+        torch.cuda.synchronize()
+        return got.cpu().double()[0]
+
+    exact = odd * up.double()
+    large, small = up.double() > 1, up.double() < 1
+    assert not bool(torch.isfinite(dx(2.0 ** 3)).any())               # dp of 2^17: infinite, and NaN times w's zeros
+    assert torch.equal(dx(2.0 ** -2)[large], exact[large] * 2.0 ** -2)
+    assert torch.equal(dx(2.0 ** -12)[small], up.double()[small] * 2.0 ** -12)  # the last digit is lost
+    assert torch.equal(dx(1.0)[small], exact[small])
