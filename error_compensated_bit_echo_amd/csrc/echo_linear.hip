@@ -476,7 +476,8 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
   char* const px = (char*)workspace + b.dp_bytes;
   char* const pw = px + b.x_bytes;
   float* const part = (float*)(pw + b.w_bytes);
-  const bool own_dp = b.dp_bytes > 0, pack = b.x_bytes + b.w_bytes > 0;
+  // (a gated call without rows has a dp of no bytes too, twice as wide as dout)
+  const bool own_dp = b.ld_dp > 0, pack = b.x_bytes + b.w_bytes > 0;
   const bool want_dp = own_dp && (dx || dw);
   if (some && (want_dp || dbias)) {
     SlopeArgs a = {};
