@@ -1,4 +1,5 @@
-"""Thin Python binding of libecho (include/echo.h, include/echo_layer.h).
+"""Thin Python binding of libecho (include/echo.h, include/echo_layer.h,
+include/echo_fp8.h).
 
 Argument marshalling only: every step of the pipeline runs in the HIP
 kernels of libecho.so.  PyTorch provides device memory and streams: tensors
@@ -57,6 +58,18 @@ class EchoLinearDescC(C.Structure):
                 ("act", C.c_int32), ("gated", C.c_int32), ("reserved", C.c_int32)]
 
 
+class EchoPack8DescC(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("ld_x", C.c_int64), ("ld_c", C.c_int64),
+                ("ld_t", C.c_int64), ("dtype", C.c_int32), ("format", C.c_int32), ("blocks", C.c_int32),
+                ("parts", C.c_int32)]
+
+
+class EchoLinear8DescC(C.Structure):
+    _fields_ = [("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64), ("ld_x", C.c_int64),
+                ("ld_w", C.c_int64), ("ld_out", C.c_int64), ("ld_r", C.c_int64), ("ld_p", C.c_int64),
+                ("dtype", C.c_int32), ("act", C.c_int32), ("gated", C.c_int32), ("x_format", C.c_int32)]
+
+
 _vp = C.c_void_p
 _pp = C.POINTER(C.c_void_p)
 _SIGNATURES = {
@@ -93,17 +106,28 @@ _LAYER_SIGNATURES = {
     "echo_linear_backward_workspace": [C.POINTER(EchoLinearDescC)],
     "echo_linear_backward": [C.POINTER(EchoLinearDescC)] + [_vp] * 8 + [C.c_int64, _vp],
 }
+# include/echo_fp8.h: the layer operators in 8-bit floating point
+_FP8_SIGNATURES = {
+    "echo_pack8": [C.POINTER(EchoPack8DescC)] + [_vp] * 6,
+    "echo_unpack8": [C.POINTER(EchoPack8DescC)] + [_vp] * 4,
+    "echo_linear8_workspace": [C.POINTER(EchoLinear8DescC)],
+    "echo_linear8": [C.POINTER(EchoLinear8DescC)] + [_vp] * 9 + [C.c_int64, _vp],
+    "echo_linear_backward8_workspace": [C.POINTER(EchoLinear8DescC)],
+    "echo_linear_backward8": [C.POINTER(EchoLinear8DescC)] + [_vp] * 10 + [C.c_int64, _vp],
+}
 _RETURNS = {"echo_status_string": C.c_char_p, "echo_norm_backward_workspace": C.c_int64,
-            "echo_linear_workspace": C.c_int64, "echo_linear_backward_workspace": C.c_int64}
+            "echo_linear_workspace": C.c_int64, "echo_linear_backward_workspace": C.c_int64,
+            "echo_linear8_workspace": C.c_int64, "echo_linear_backward8_workspace": C.c_int64}
 EXPORTED = tuple(_SIGNATURES)
 EXPORTED_LAYER = tuple(_LAYER_SIGNATURES)
+EXPORTED_FP8 = tuple(_FP8_SIGNATURES)
 
 
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libecho.so not built at {LIB_PATH}; run __graft_entry__.build()")
     lib = C.CDLL(LIB_PATH)
-    for name, args in {**_SIGNATURES, **_LAYER_SIGNATURES}.items():
+    for name, args in {**_SIGNATURES, **_LAYER_SIGNATURES, **_FP8_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = _RETURNS.get(name, C.c_int)
@@ -622,6 +646,175 @@ def echo_linear_backward(dout, x, w, p, dx, dw, *, dbias=None, act="none", gated
                                     _dense(dx, (m, k), dt, "dx"), _dense(dw, (rows, k), dt, "dw"),
                                     _dense(dbias, (rows,), dt, "dbias"), sp, sn, _stream(stream)),
            "echo_linear_backward")
+
+
+# ---- layer operators in 8-bit floating point ---------------------------------------
+
+FORMATS = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
+BLOCK = 128
+
+
+def _blocks(n):
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _codes(t, rows, cols, what, formats=FORMATS):
+    """(address, row pitch, format) of a [rows, cols] matrix of 8-bit codes whose
+    rows have unit stride and begin at multiples of 16 bytes"""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in formats and t.dim() > 0 and t.shape[-1] == cols \
+            and t.numel() == rows * cols:
+        at, pitch = t.data_ptr(), 0
+        if rows > 1 and cols:
+            if t.dim() == 2:
+                pitch, unit = t.stride()
+                dense = cols <= 1 or unit == 1
+            else:
+                pitch, dense = cols, t.is_contiguous()
+            dense = dense and pitch >= cols and pitch % 16 == 0
+        else:
+            dense = t.is_contiguous()
+        if dense and at % 16 == 0:
+            return at, pitch, formats[t.dtype]
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: a tensor of codes is required")
+    if t.dtype not in formats:
+        raise ValueError(f"{what}: {' or '.join(map(str, formats))} is required (got {t.dtype})")
+    bad = _bad_tensor(t, (rows, cols), t.dtype, what)
+    raise ValueError(bad or f"{what}: rows of unit stride that do not overlap, each at a multiple of 16 bytes, are "
+                            f"required (strides {t.stride()}); codes8_empty makes such a tensor")
+
+
+_E4M3 = {torch.float8_e4m3fn: 3}
+
+
+def codes8_empty(rows, cols, dtype=torch.float8_e4m3fn, device="cuda"):
+    """an uninitialised [rows, cols] matrix of 8-bit codes whose rows begin at
+    multiples of 16 bytes, as the calls below need them"""
+    return torch.empty(rows, (cols + 15) // 16 * 16, dtype=dtype, device=device)[:, :cols]
+
+
+def scales8_shape(rows, cols, *, blocks=False, parts=1):
+    """shape of the binary32 scales beside a [rows, cols] matrix of codes"""
+    if blocks:
+        return parts * _blocks(rows // parts), _blocks(cols)
+    return rows, parts * _blocks(cols // parts)
+
+
+def _pack8_desc(x, codes, blocks, parts, what):
+    """(descriptor, address of x, address of codes, shape of the scales)"""
+    rows, cols = _rows_of(x, what)
+    xp, ldx = _matrix(x, rows, cols, x.dtype, what)
+    cp, ldc, fmt = _codes(codes, rows, cols, "codes")
+    d = EchoPack8DescC(rows, cols, ldx, ldc, 0, DTYPES[x.dtype], fmt, 1 if blocks else 0, int(parts))
+    return d, xp, cp, scales8_shape(rows, cols, blocks=blocks, parts=parts if parts in (1, 2) else 1)
+
+
+def echo_pack8(x, codes, scales, *, blocks=False, parts=1, codes_t=None, scales_t=None, stream=None) -> None:
+    """codes = x / scales, one binary32 scale, a power of two, for each block of
+    128 elements of a row, or with blocks of 128 x 128.
+
+    x [rows, cols] bfloat16, float16 or float32; codes float8_e4m3fn or
+    float8_e5m2 (codes8_empty); scales float32 (scales8_shape).  parts = 2: the
+    blocks begin anew at the second half of the columns, or with blocks of the
+    rows (a gated product's sums and weights).  codes_t [cols, rows] and scales_t
+    take the transposed matrix, of blocks only."""
+    d, xp, cp, shape = _pack8_desc(x, codes, blocks, parts, "x")
+    tp = None
+    if codes_t is not None:
+        tp, d.ld_t, fmt = _codes(codes_t, d.cols, d.rows, "codes_t")
+        if fmt != d.format:
+            raise ValueError(f"codes_t: {codes.dtype} is required (got {codes_t.dtype})")
+    rc = lib.echo_pack8(C.byref(d), xp, cp, _dense(scales, shape, torch.float32, "scales"), tp,
+                        scales_t if scales_t is None else _dense(scales_t, shape[::-1], torch.float32, "scales_t"),
+                        _stream(stream))
+    if rc:
+        _check(rc, "echo_pack8")
+
+
+def echo_unpack8(codes, scales, x, *, blocks=False, parts=1, stream=None) -> None:
+    """x = codes times scales, rounded to x's type (arguments as in echo_pack8)"""
+    d, xp, cp, shape = _pack8_desc(x, codes, blocks, parts, "x")
+    rc = lib.echo_unpack8(C.byref(d), cp, _dense(scales, shape, torch.float32, "scales"), xp, _stream(stream))
+    if rc:
+        _check(rc, "echo_unpack8")
+
+
+def _linear8_desc(m, n, k, act, gated, dtype=0, ld_x=0, ld_w=0, ld_out=0, ld_r=0, ld_p=0, x_format=3):
+    return EchoLinear8DescC(int(m), int(n), int(k), ld_x, ld_w, ld_out, ld_r, ld_p, dtype, _code(ACTS, act, "act"),
+                            1 if gated else 0, x_format)
+
+
+def echo_linear8_workspace(m, n, k, act="none", gated=False) -> int:
+    """bytes of workspace echo_linear8 takes for m rows of x, n outputs, k inputs"""
+    r = lib.echo_linear8_workspace(C.byref(_linear8_desc(m, n, k, act, gated)))
+    _check(min(r, 0), "echo_linear8_workspace")
+    return r
+
+
+def echo_linear_backward8_workspace(m, n, k, act="none", gated=False) -> int:
+    """bytes of workspace echo_linear_backward8 takes for this shape"""
+    r = lib.echo_linear_backward8_workspace(C.byref(_linear8_desc(m, n, k, act, gated)))
+    _check(min(r, 0), "echo_linear_backward8_workspace")
+    return r
+
+
+def _linear8_shape(x, w, like, gated):
+    """(m, n, k, rows of w, type of `like`)"""
+    if not isinstance(x, torch.Tensor) or x.dim() == 0:
+        raise ValueError("x: a tensor of codes is required")
+    k = x.shape[-1]
+    m = x.numel() // k if k else math.prod(x.shape[:-1])
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or (gated and w.shape[0] % 2):
+        raise ValueError("w: a matrix is required, with an even number of rows if the product is gated")
+    if not isinstance(like, torch.Tensor) or like.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("out, dout: a bfloat16 or float16 tensor is required")
+    rows = w.shape[0]
+    return m, (rows // 2 if gated else rows), k, rows, like.dtype
+
+
+def echo_linear8(x, sx, w, sw, out, *, bias=None, residual=None, act="none", gated=False, p=None, workspace=None,
+                 stream=None) -> None:
+    """echo_linear with x and w in 8 bits: out = act(p) + residual for p = x w^T +
+    bias, gated out = act(p_gate) * p_up + residual.
+
+    x [m, k] codes with scales sx for each 128 of a row; w [n, k] (gated [2n, k])
+    float8_e4m3fn with scales sw for each 128 x 128 (gated, of two parts); out,
+    residual [m, n], bias and p (dense) bfloat16 or float16."""
+    m, n, k, rows, dt = _linear8_shape(x, w, out, gated)
+    xp, ldx, fmt = _codes(x, m, k, "x")
+    wp, ldw, _ = _codes(w, rows, k, "w", _E4M3)
+    op, ldo = _matrix(out, m, n, dt, "out")
+    rp, ldr = _matrix(residual, m, n, dt, "residual") if residual is not None else (None, 0)
+    d = _linear8_desc(m, n, k, act, gated, DTYPES[dt], ldx, ldw, ldo, ldr, 0, fmt)
+    sp, sn = _workspace(workspace)
+    rc = lib.echo_linear8(C.byref(d), xp, _dense(sx, (m, _blocks(k)), torch.float32, "sx"), wp,
+                          _dense(sw, ((2 if gated else 1) * _blocks(n), _blocks(k)), torch.float32, "sw"),
+                          bias if bias is None else _dense(bias, (rows,), dt, "bias"), rp, op,
+                          p if p is None else _dense(p, (m, rows), dt, "p"), sp, sn, _stream(stream))
+    if rc:
+        _check(rc, "echo_linear8")
+
+
+def echo_linear_backward8(dout, x, sx, w, p, sp, dx, dw, *, dbias=None, act="none", gated=False, workspace=None,
+                          stream=None) -> None:
+    """echo_linear_backward from checkpoints in 8 bits: the forward call's x
+    (codes, scales sx for each 128 of a row) and p (float8_e4m3fn, scales sp for
+    each 128 of a row, gated of two parts; None without an activation and a
+    gate); dout, w and the gradients are bfloat16 or float16."""
+    m, n, k, rows, dt = _linear8_shape(x, w, dout, gated)
+    gp, ldo = _matrix(dout, m, n, dt, "dout")
+    xp, ldx, fmt = _codes(x, m, k, "x")
+    wp, ldw = _matrix(w, rows, k, dt, "w")
+    pp, ldp, _ = (None, 0, 0) if p is None else _codes(p, m, rows, "p", _E4M3)
+    d = _linear8_desc(m, n, k, act, gated, DTYPES[dt], ldx, ldw, ldo, 0, ldp, fmt)
+    wsp, wsn = _workspace(workspace)
+    rc = lib.echo_linear_backward8(
+        C.byref(d), gp, xp, _dense(sx, (m, _blocks(k)), torch.float32, "sx"), wp, pp,
+        sp if sp is None else _dense(sp, (m, (2 if gated else 1) * _blocks(n)), torch.float32, "sp"),
+        _dense(dx, (m, k), dt, "dx"), _dense(dw, (rows, k), dt, "dw"), _dense(dbias, (rows,), dt, "dbias"), wsp, wsn,
+        _stream(stream))
+    if rc:
+        _check(rc, "echo_linear_backward8")
 
 
 def echo_get_config() -> dict:

@@ -1,14 +1,17 @@
 // echo_linear.hip -- matrix products with bias, activation and residual in the
 // epilogue, and their gradients: the host side of echo_linear and
-// echo_linear_backward (include/echo_layer.h) and the kernels beside the tile
-// kernel of linear_tile.h.
+// echo_linear_backward (include/echo_layer.h) and of echo_linear_backward8
+// (include/echo_fp8.h), and the kernels beside the tile kernel of linear_tile.h.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "echo_layer.h"
+#include "fp8_device.h"
+#include "fp8_host.h"
 #include "host_checks.h"
 #include "linear_device.h"
+#include "linear_join.h"
 #include "linear_tile.h"
 
 using namespace echo;
@@ -30,6 +33,8 @@ namespace {
 struct SlopeArgs {
   const void *dout;
   const void* p;  // nullable: no activation, dp is a copy of dout
+  const float* sp;  // p in 8 bits: its scales, ld_sp to a row
+  int64_t ld_p, ld_sp;  // p in 8 bits: row pitches (else p is dense)
   void* dp;       // nullable: dp is dout itself; rows filled up with zeros to ld_dp
   float* part;    // nullable: [runs][columns of dp] sums
   int64_t m, n, ld_out, ld_dp, run;
@@ -40,7 +45,9 @@ struct SlopeArgs {
 // would be waited for.  WHOLE: rows are whole vectors.  Otherwise a row's last
 // vector is read as the row's last eight elements and moved down, and rows
 // under a vector are read element by element.
-template <typename T, bool GATED, bool WHOLE>
+// P8: p is e4m3 codes with a scale for each 128, gated of two parts; eight codes are
+// read as they lie, since a row's pitch holds its length rounded up to 16.
+template <typename T, bool GATED, bool WHOLE, bool P8>
 __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
   __shared__ float lds[GATED ? 2 : 1][256 * 8 + 32 * 8];
   const int tx = threadIdx.x & (a.wide - 1), ty = threadIdx.x / a.wide, high = 256 / a.wide;
@@ -79,13 +86,29 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
     }
   };
   const int back = !WHOLE && n < 8 ? 8 - n : 0;
+  auto fetch_codes = [&](int64_t r, int part, u32x2& c, float& scale) {
+    c = __builtin_nontemporal_load((const u32x2_a1*)((const uint8_t*)a.p + r * a.ld_p + part * a.n + col));
+    scale = a.sp[r * a.ld_sp + (part ? a.ld_sp / 2 : 0) + col / ECHO_FP8_BLOCK];
+  };
+  auto scaled = [&](u32x2 c, float scale, float (&f)[8]) {
+    values_of<ECHO_E4M3>(c, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = value_of<float>(f[e], scale);
+  };
   if ((WHOLE || a.n >= 8) && n > 0) {
     for (int64_t r = r0 + ty; r < r1; r += 2 * high) {
       Raw<T> d[2], p[2], u[2];
+      u32x2 cp[2], cu[2];
+      float sp[2], su8[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // past the end the last row once more
         const int64_t at = min(r + k * high, r1 - 1);
         d[k] = fetch_at<true>((const T*)a.dout + at * a.ld_out + col - back);
+        if constexpr (P8) {
+          fetch_codes(at, 0, cp[k], sp[k]);
+          if (GATED) fetch_codes(at, 1, cu[k], su8[k]);
+          continue;
+        }
         if (a.p) p[k] = fetch_at<true>((const T*)a.p + at * cols + col - back);
         if (GATED && a.p) u[k] = fetch_at<true>((const T*)a.p + at * cols + a.n + col - back);
       }
@@ -93,14 +116,19 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
       for (int k = 0; k < 2; ++k) {
         if (r + k * high >= r1) continue;
         float fd[8], fp[8], fu[8];
-        if constexpr (!WHOLE) {
-          MoveDown{back}(d[k]);
-          if (a.p) MoveDown{back}(p[k]);
-          if (GATED && a.p) MoveDown{back}(u[k]);
-        }
+        if constexpr (!WHOLE) MoveDown{back}(d[k]);
         unpack_raw(d[k], fd);
-        if (a.p) unpack_raw(p[k], fp);
-        if (GATED && a.p) unpack_raw(u[k], fu);
+        if constexpr (P8) {
+          scaled(cp[k], sp[k], fp);
+          if (GATED) scaled(cu[k], su8[k], fu);
+        } else {
+          if constexpr (!WHOLE) {
+            if (a.p) MoveDown{back}(p[k]);
+            if (GATED && a.p) MoveDown{back}(u[k]);
+          }
+          if (a.p) unpack_raw(p[k], fp);
+          if (GATED && a.p) unpack_raw(u[k], fu);
+        }
         row(r + k * high, fd, fp, fu);
       }
     }
@@ -108,7 +136,16 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
     for (int64_t r = r0 + ty; r < r1; r += high) {
       float d[8], p[8], u[8];
       load_n<true>((const T*)a.dout + r * a.ld_out + col, n, d);
-      if (a.p) {
+      if constexpr (P8) {
+        u32x2 c;
+        float sc;
+        fetch_codes(r, 0, c, sc);
+        scaled(c, sc, p);
+        if (GATED) {
+          fetch_codes(r, 1, c, sc);
+          scaled(c, sc, u);
+        }
+      } else if (a.p) {
         load_n<true>((const T*)a.p + r * cols + col, n, p);
         if (GATED) load_n<true>((const T*)a.p + r * cols + a.n + col, n, u);
       }
@@ -187,34 +224,6 @@ __global__ __launch_bounds__(1024) void k_run_sum(RunSumArgs a) {
 #pragma unroll
     for (int i = 1; i < 32; ++i) s += lds[i][c];
     ((T*)a.out)[col] = from_f32<T>(s);
-  }
-}
-
-// ---- joining splits ---------------------------------------------------------------
-// The splits' sums added in order, then the epilogue; 8 outputs to a thread.
-template <typename T, bool GATED>
-__global__ __launch_bounds__(kBlock) void k_join(TileArgs a) {
-  const int64_t cols = GATED ? 2 * a.J : a.J, vectors = (a.J + 7) / 8;
-  const int64_t plane = a.I * cols, items = a.I * vectors;
-  for (int64_t t = (int64_t)blockIdx.x * kBlock + threadIdx.x; t < items; t += (int64_t)gridDim.x * kBlock) {
-    const int64_t i = t / vectors, j = (t - i * vectors) * 8;
-    const int n = (int)min(a.J - j, (int64_t)8);
-    const float* p = a.part + i * cols + j;
-    float g[8], u[8], f[8];
-    load_n<true>(p, n, g);
-    if (GATED) load_n<true>(p + a.J, n, u);
-    for (uint32_t s = 1; s < a.splits; ++s) {
-      p += plane;
-      load_n<true>(p, n, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] += f[e];
-      if (GATED) {
-        load_n<true>(p + a.J, n, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] += f[e];
-      }
-    }
-    finish<T, 8, GATED>(a, i, j, n, g, u);
   }
 }
 
@@ -297,18 +306,13 @@ int64_t forward_bytes(const Geometry& g) {
   return copies + part_bytes(g.m, g.rows, g.k);
 }
 
-template <bool GATED>
-int run_join(const TileArgs& a, int32_t dtype, hipStream_t s) {
-  const uint64_t items = (uint64_t)a.I * (uint64_t)((a.J + 7) / 8);
-  const dim3 grid(blocks_for_items(items)), block(kBlock);
-  return dtype == ECHO_BF16 ? launch(k_join<bf16_t, GATED>, grid, block, s, a)
-                            : launch(k_join<f16_t, GATED>, grid, block, s, a);
-}
-
 template <typename T, bool GATED>
 int run_slope(const SlopeArgs& a, dim3 grid, dim3 block, hipStream_t s) {
-  return a.n % 8 ? launch(k_slope<T, GATED, false>, grid, block, s, a)
-                 : launch(k_slope<T, GATED, true>, grid, block, s, a);
+  if (a.sp)
+    return a.n % 8 ? launch(k_slope<T, GATED, false, true>, grid, block, s, a)
+                   : launch(k_slope<T, GATED, true, true>, grid, block, s, a);
+  return a.n % 8 ? launch(k_slope<T, GATED, false, false>, grid, block, s, a)
+                 : launch(k_slope<T, GATED, true, false>, grid, block, s, a);
 }
 
 void apply(const Plan& p, void* part, TileArgs& a) {
@@ -319,7 +323,8 @@ void apply(const Plan& p, void* part, TileArgs& a) {
 
 // The backward pass's workspace: dp where it differs from dout, copies of dout,
 // x and w with whole rows where those pay, the bias's partial sums, one row for
-// each run of rows, and the splits' sums.
+// each run of rows, and the splits' sums.  From checkpoints in 8 bits x's copy is x
+// unpacked, with whole rows.
 struct BackPlan {
   bool copies;
   int32_t wide;
@@ -327,18 +332,24 @@ struct BackPlan {
   int64_t bytes() const { return dp_bytes + x_bytes + w_bytes + bias_bytes + split_bytes; }
 };
 
-BackPlan plan_back(const echo_linear_desc* d, const Geometry& g) {
+BackPlan plan_back(const Geometry& g, bool slope, bool eight) {
   BackPlan b = {};
-  const bool slope = d->act != ECHO_ACT_NONE || d->gated;
   const bool odd_k = g.k % 8 != 0, odd_n = !slope && g.n % 8 != 0;
-  if (odd_k || odd_n) {
+  if (eight) {
+    b.x_bytes = copy_bytes(g.m, g.k);
+    const double copied = plan_tiles(g.m, g.k, g.rows, true).us, staged = plan_tiles(g.m, g.k, g.rows, false).us;
+    const double odd_dw = plan_tiles(g.rows, g.k, g.m, false).us - plan_tiles(g.rows, g.k, g.m, true).us;
+    const double cost = (odd_k ? copy_us(copy_bytes(g.rows, g.k)) : 0.0) + (odd_n ? copy_us(copy_bytes(g.m, g.n)) : 0.0);
+    b.copies = (odd_k || odd_n) && copied + cost < staged + (odd_n ? odd_dw : 0.0);
+    if (b.copies && odd_k) b.w_bytes = copy_bytes(g.rows, g.k);
+  } else if (odd_k || odd_n) {
     const double copied = plan_tiles(g.m, g.k, g.rows, true).us + plan_tiles(g.rows, g.k, g.m, true).us;
     const double staged = plan_tiles(g.m, g.k, g.rows, false).us + plan_tiles(g.rows, g.k, g.m, false).us;
     const double cost = (odd_k ? copy_us(copy_bytes(g.m + g.rows, g.k)) : 0.0) +
                         (odd_n ? copy_us(copy_bytes(g.m, g.n)) : 0.0);
     b.copies = copied + cost < staged;
   }
-  if (b.copies && odd_k) {
+  if (!eight && b.copies && odd_k) {
     b.x_bytes = copy_bytes(g.m, g.k);
     b.w_bytes = copy_bytes(g.rows, g.k);
   }
@@ -358,6 +369,94 @@ BackPlan plan_back(const echo_linear_desc* d, const Geometry& g) {
   const int64_t dx = part_bytes(g.m, g.k, g.rows), dw = part_bytes(g.rows, g.k, g.m);
   b.split_bytes = dx > dw ? dx : dw;  // one after the other on the stream
   return b;
+}
+
+Geometry geometry_of(const Shape8& h, const echo_linear8_desc* d) {
+  return {h.m, h.n, h.k, h.rows, h.ld_x, d->ld_w ? d->ld_w : h.k, h.ld_out, h.n};
+}
+
+struct How { int32_t dtype, act, gated, x_format; };  // x_format: -1 if x and p are of dtype
+
+// The launches of both backward calls, arguments checked.  `from` has p; x in 8 bits
+// has scales sx.
+int run_backward(How how, const Geometry& g, const BackPlan& b, const void* dout, const SlopeArgs& from, const void* x,
+                 const float* sx, const void* w, void* dx, void* dw, void* dbias, void* workspace, hipStream_t s) {
+  int rc = ECHO_SUCCESS;
+  const bool eight = how.x_format >= 0;
+  const bool bf16 = how.dtype == ECHO_BF16, some = g.m > 0 && g.n > 0;
+  char* const px = (char*)workspace + b.dp_bytes;
+  char* const pw = px + b.x_bytes;
+  float* const part = (float*)(pw + b.w_bytes);
+  // (a gated call without rows has a dp of no bytes too, twice as wide as dout)
+  const bool own_dp = b.ld_dp > 0;
+  const bool want_dp = own_dp && (dx || dw);
+  if (some && (want_dp || dbias)) {
+    SlopeArgs a = from;
+    a.dout = dout;
+    a.dp = want_dp ? workspace : nullptr;
+    a.part = dbias ? part : nullptr;
+    a.m = g.m;
+    a.n = g.n;
+    a.ld_out = g.ld_out;
+    a.ld_dp = b.ld_dp;
+    a.run = b.run;
+    a.act = how.act;
+    a.gated = how.gated;
+    a.wide = b.wide;
+    const dim3 grid((uint32_t)((g.n + b.wide * 8 - 1) / (b.wide * 8)), (uint32_t)b.runs), block(256);
+    if (how.gated)
+      rc = bf16 ? run_slope<bf16_t, true>(a, grid, block, s) : run_slope<f16_t, true>(a, grid, block, s);
+    else
+      rc = bf16 ? run_slope<bf16_t, false>(a, grid, block, s) : run_slope<f16_t, false>(a, grid, block, s);
+    if (rc) return rc;
+  }
+  if (dbias && g.rows > 0) {
+    RunSumArgs a = {part, dbias, g.rows, some ? (uint32_t)b.runs : 0};
+    const dim3 grid((uint32_t)((g.rows + 31) / 32)), block(1024);
+    rc = bf16 ? launch(k_run_sum<bf16_t>, grid, block, s, a) : launch(k_run_sum<f16_t>, grid, block, s, a);
+    if (rc) return rc;
+  }
+  TileArgs a = {};
+  a.a = own_dp ? workspace : dout;
+  a.lda = own_dp ? b.ld_dp : g.ld_out;
+  a.padded = own_dp;
+  void* const splits = (char*)part + b.bias_bytes;
+  if (some && eight && dw) {
+    rc = unpack_rows(x, g.ld_x, sx, how.x_format, g.m, g.k, px, round_up(g.k, 8), how.dtype, s);
+    if (rc) return rc;
+  }
+  if (some && (b.w_bytes > 0 || (b.x_bytes > 0 && !eight))) {
+    rc = run_pack(g, dw && !eight ? x : nullptr, px, dx ? w : nullptr, pw, how.dtype, s);
+    if (rc) return rc;
+  }
+  if (dx) {
+    a.b = b.w_bytes ? pw : w;
+    a.ldb = b.w_bytes ? round_up(g.k, 8) : g.ld_w;
+    a.I = g.m;
+    a.J = g.k;
+    a.C = g.rows;
+    a.out = dx;
+    a.ldo = g.k;
+    const Plan plan = plan_tiles(a.I, a.J, a.C, chunked<false, true>(a));
+    apply(plan, splits, a);
+    rc = tile_dx(a, how.dtype, plan.tile, s);
+    if (!rc && plan.splits > 1) rc = run_join<false>(a, how.dtype, s);
+    if (rc) return rc;
+  }
+  if (dw) {
+    a.b = b.x_bytes ? px : x;
+    a.ldb = b.x_bytes ? round_up(g.k, 8) : g.ld_x;
+    a.I = g.rows;
+    a.J = g.k;
+    a.C = g.m;
+    a.out = dw;
+    a.ldo = g.k;
+    const Plan plan = plan_tiles(a.I, a.J, a.C, chunked<true, true>(a));
+    apply(plan, splits, a);
+    rc = tile_dw(a, how.dtype, plan.tile, s);
+    if (!rc && plan.splits > 1) rc = run_join<false>(a, how.dtype, s);
+  }
+  return rc;
 }
 
 }  // namespace
@@ -435,7 +534,7 @@ int64_t echo_linear_backward_workspace(const echo_linear_desc* d) {
   Geometry g;
   const int rc = check_desc(d, g);
   if (rc) return rc;
-  const BackPlan b = plan_back(d, g);
+  const BackPlan b = plan_back(g, d->act != ECHO_ACT_NONE || d->gated, false);
   return b.bytes();
 }
 
@@ -451,7 +550,7 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
     if (!dout || (slope && !p)) return ECHO_ERR_INVALID_ARGUMENT;
     if (g.k > 0 && ((dx && !w) || (dw && !x))) return ECHO_ERR_INVALID_ARGUMENT;
   }
-  const BackPlan b = plan_back(d, g);
+  const BackPlan b = plan_back(g, slope, false);
   const int64_t need = b.bytes();
   if (need > 0) {
     if (!workspace) return ECHO_ERR_INVALID_ARGUMENT;
@@ -471,78 +570,70 @@ int echo_linear_backward(const echo_linear_desc* d, const void* dout, const void
   if (slope) al.in(p, g.m * g.rows * 2);
   if (!al.ok()) return ECHO_ERR_ALIAS;
 
-  const hipStream_t s = (hipStream_t)stream;
-  const bool bf16 = d->dtype == ECHO_BF16;
-  char* const px = (char*)workspace + b.dp_bytes;
-  char* const pw = px + b.x_bytes;
-  float* const part = (float*)(pw + b.w_bytes);
-  // (a gated call without rows has a dp of no bytes too, twice as wide as dout)
-  const bool own_dp = b.ld_dp > 0, pack = b.x_bytes + b.w_bytes > 0;
-  const bool want_dp = own_dp && (dx || dw);
-  if (some && (want_dp || dbias)) {
-    SlopeArgs a = {};
-    a.dout = dout;
-    a.p = slope ? p : nullptr;
-    a.dp = want_dp ? workspace : nullptr;
-    a.part = dbias ? part : nullptr;
-    a.m = g.m;
-    a.n = g.n;
-    a.ld_out = g.ld_out;
-    a.ld_dp = b.ld_dp;
-    a.run = b.run;
-    a.act = d->act;
-    a.gated = d->gated;
-    a.wide = b.wide;
-    const dim3 grid((uint32_t)((g.n + b.wide * 8 - 1) / (b.wide * 8)), (uint32_t)b.runs), block(256);
-    if (d->gated)
-      rc = bf16 ? run_slope<bf16_t, true>(a, grid, block, s) : run_slope<f16_t, true>(a, grid, block, s);
-    else
-      rc = bf16 ? run_slope<bf16_t, false>(a, grid, block, s) : run_slope<f16_t, false>(a, grid, block, s);
-    if (rc) return rc;
+  SlopeArgs from = {};
+  from.p = slope ? p : nullptr;
+  return run_backward({d->dtype, d->act, d->gated, -1}, g, b, dout, from, x, nullptr, w, dx, dw, dbias, workspace,
+                      (hipStream_t)stream);
+}
+
+int64_t echo_linear_backward8_workspace(const echo_linear8_desc* d) {
+  Shape8 h;
+  const int rc = check_shape8(d, h);
+  if (rc) return rc;
+  return plan_back(geometry_of(h, d), d->act != ECHO_ACT_NONE || d->gated, true).bytes();
+}
+
+int echo_linear_backward8(const echo_linear8_desc* d, const void* dout, const void* x,
+                          const float* sx, const void* w, const void* p, const float* sp, void* dx,
+                          void* dw, void* dbias, void* workspace, int64_t workspace_bytes,
+                          echo_stream_t stream) {
+  Shape8 h;
+  int rc = check_shape8(d, h);
+  if (rc) return rc;
+  const Geometry g = geometry_of(h, d);
+  if (d->ld_w != 0 && (d->ld_w < g.k || d->ld_w > ECHO_MAX_PITCH)) return ECHO_ERR_SHAPE;
+  const bool slope = d->act != ECHO_ACT_NONE || d->gated;
+  int64_t ld_p = 0;
+  if (slope) rc = code_pitch(d->ld_p, g.rows, ld_p);
+  if (rc) return rc;
+  const bool some = g.m > 0 && g.n > 0;
+  if (some && (dx || dw || dbias)) {
+    if (!dout || (slope && (!p || !sp))) return ECHO_ERR_INVALID_ARGUMENT;
+    if (g.k > 0 && ((dx && !w) || (dw && (!x || !sx)))) return ECHO_ERR_INVALID_ARGUMENT;
   }
-  if (dbias && g.rows > 0) {
-    RunSumArgs a = {part, dbias, g.rows, some ? (uint32_t)b.runs : 0};
-    const dim3 grid((uint32_t)((g.rows + 31) / 32)), block(1024);
-    rc = bf16 ? launch(k_run_sum<bf16_t>, grid, block, s, a) : launch(k_run_sum<f16_t>, grid, block, s, a);
-    if (rc) return rc;
+  const BackPlan b = plan_back(g, slope, true);
+  const int64_t need = b.bytes(), groups = (d->gated ? 2 : 1) * blocks_of(g.n);
+  if (need > 0) {
+    if (!workspace) return ECHO_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return ECHO_ERR_WORKSPACE;
   }
-  TileArgs a = {};
-  a.a = own_dp ? workspace : dout;
-  a.lda = own_dp ? b.ld_dp : g.ld_out;
-  a.padded = own_dp;
-  void* const splits = (char*)part + b.bias_bytes;
-  if (pack && some) {
-    rc = run_pack(g, dw ? x : nullptr, px, dx ? w : nullptr, pw, d->dtype, s);
-    if (rc) return rc;
+  for (const void* q : {dout, w, (const void*)dx, (const void*)dw, (const void*)dbias})
+    if (!aligned(q, 2)) return ECHO_ERR_ALIGNMENT;
+  if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(sx, 4)) return ECHO_ERR_ALIGNMENT;
+  if (slope && (!aligned(p, 16) || !aligned(sp, 4))) return ECHO_ERR_ALIGNMENT;
+  Aliases al;
+  al.out(dx, g.m * g.k * 2);
+  al.out(dw, g.rows * g.k * 2);
+  al.out(dbias, g.rows * 2);
+  al.out(workspace, need);
+  al.in(dout, span(g.m, g.n, g.ld_out));
+  al.in(x, bytes_of(g.m, g.k, g.ld_x, 1));
+  al.in(sx, g.m * blocks_of(g.k) * 4);
+  al.in(w, span(g.rows, g.k, g.ld_w));
+  if (slope) {
+    al.in(p, bytes_of(g.m, g.rows, ld_p, 1));
+    al.in(sp, g.m * groups * 4);
   }
-  if (dx) {
-    a.b = pack ? pw : w;
-    a.ldb = pack ? round_up(g.k, 8) : g.ld_w;
-    a.I = g.m;
-    a.J = g.k;
-    a.C = g.rows;
-    a.out = dx;
-    a.ldo = g.k;
-    const Plan plan = plan_tiles(a.I, a.J, a.C, chunked<false, true>(a));
-    apply(plan, splits, a);
-    rc = tile_dx(a, d->dtype, plan.tile, s);
-    if (!rc && plan.splits > 1) rc = run_join<false>(a, d->dtype, s);
-    if (rc) return rc;
+  if (!al.ok()) return ECHO_ERR_ALIAS;
+  SlopeArgs from = {};
+  if (slope) {
+    from.p = p;
+    from.sp = sp;
+    from.ld_p = ld_p;
+    from.ld_sp = groups;
   }
-  if (dw) {
-    a.b = pack ? px : x;
-    a.ldb = pack ? round_up(g.k, 8) : g.ld_x;
-    a.I = g.rows;
-    a.J = g.k;
-    a.C = g.m;
-    a.out = dw;
-    a.ldo = g.k;
-    const Plan plan = plan_tiles(a.I, a.J, a.C, chunked<true, true>(a));
-    apply(plan, splits, a);
-    rc = tile_dw(a, d->dtype, plan.tile, s);
-    if (!rc && plan.splits > 1) rc = run_join<false>(a, d->dtype, s);
-  }
-  return rc;
+  return run_backward({d->dtype, d->act, d->gated, d->x_format}, g, b, dout, from, x, sx, w, dx, dw, dbias, workspace,
+                      (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -31,11 +31,12 @@ constexpr int64_t kMostPart = INT64_C(256) << 20;  // bytes of partial sums
 
 struct Plan { int tile; int64_t splits, chunk, part_bytes; double us; };
 
-inline Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
-  const int64_t steps = (C + kC - 1) / kC;
-  Plan best = {kTile64, 1, steps * kC, 0, 1e30};
+// `depth`: contraction length of a step
+inline Plan plan_by(const TileCost (&costs)[kTileKinds], int depth, int64_t I, int64_t cols, int64_t C) {
+  const int64_t steps = (C + depth - 1) / depth;
+  Plan best = {kTile64, 1, steps * depth, 0, 1e30};
   for (int t = 0; t < kTileKinds; ++t) {
-    const TileCost& k = is_chunked ? kChunkedCost[t] : kStagedCost[t];
+    const TileCost& k = costs[t];
     if (k.bi == 0) continue;
     const int64_t tiles = ((I + k.bi - 1) / k.bi) * ((cols + k.bj - 1) / k.bj);
     // at least four steps to a split, and no more than four rounds of workgroups
@@ -49,10 +50,14 @@ inline Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
       const double per_cu = (double)((tiles * real + 255) / 256);
       const double shared = per_cu * ((double)each * k.step + k.over), lone = (double)each * k.alone + k.over;
       const double us = (shared > lone ? shared : lone) + (real > 1 ? 3.0 + bytes * 2.0 / 4.5e6 : 0.0);
-      if (us < best.us) best = {t, real > 0 ? real : 1, each * kC, real > 1 ? (int64_t)bytes : 0, us};
+      if (us < best.us) best = {t, real > 0 ? real : 1, each * depth, real > 1 ? (int64_t)bytes : 0, us};
     }
   }
   return best;
+}
+
+inline Plan plan_tiles(int64_t I, int64_t cols, int64_t C, bool is_chunked) {
+  return is_chunked ? plan_by(kChunkedCost, kC, I, cols, C) : plan_by(kStagedCost, kC, I, cols, C);
 }
 
 // A launch's x dimension holds at most 2^32 - 1 work-items, fewer than the small
