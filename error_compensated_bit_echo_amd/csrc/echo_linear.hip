@@ -91,9 +91,7 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
     scale = a.sp[r * a.ld_sp + (part ? a.ld_sp / 2 : 0) + col / ECHO_FP8_BLOCK];
   };
   auto scaled = [&](u32x2 c, float scale, float (&f)[8]) {
-    values_of<ECHO_E4M3>(c, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = value_of<float>(f[e], scale);
+    values_of<float, ECHO_E4M3>(c, scale, f);
   };
   if ((WHOLE || a.n >= 8) && n > 0) {
     for (int64_t r = r0 + ty; r < r1; r += 2 * high) {
