@@ -661,20 +661,19 @@ def _blocks(n):
 def _codes(t, rows, cols, what, formats=FORMATS):
     """(address, row pitch, format) of a [rows, cols] matrix of 8-bit codes whose
     rows have unit stride and begin at multiples of 16 bytes"""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in formats and t.dim() > 0 and t.shape[-1] == cols \
-            and t.numel() == rows * cols:
-        at, pitch = t.data_ptr(), 0
-        if rows > 1 and cols:
-            if t.dim() == 2:
+    if isinstance(t, torch.Tensor) and t.dtype in formats and t.is_cuda:
+        shape = t.shape
+        if len(shape) == 2 and rows > 1 and cols:  # (the smallest products cost their host time)
+            if shape[0] == rows and shape[1] == cols:
                 pitch, unit = t.stride()
-                dense = cols <= 1 or unit == 1
-            else:
-                pitch, dense = cols, t.is_contiguous()
-            dense = dense and pitch >= cols and pitch % 16 == 0
-        else:
-            dense = t.is_contiguous()
-        if dense and at % 16 == 0:
-            return at, pitch, formats[t.dtype]
+                if (unit == 1 or cols == 1) and pitch >= cols and pitch % 16 == 0:
+                    at = t.data_ptr()
+                    if at % 16 == 0:
+                        return at, pitch, formats[t.dtype]
+        elif shape and shape[-1] == cols and t.numel() == rows * cols and t.is_contiguous():
+            at = t.data_ptr()
+            if at % 16 == 0 and (rows <= 1 or cols % 16 == 0):
+                return at, (cols if rows > 1 else 0), formats[t.dtype]
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{what}: a tensor of codes is required")
     if t.dtype not in formats:
@@ -762,14 +761,17 @@ def _linear8_shape(x, w, like, gated):
     """(m, n, k, rows of w, type of `like`)"""
     if not isinstance(x, torch.Tensor) or x.dim() == 0:
         raise ValueError("x: a tensor of codes is required")
-    k = x.shape[-1]
-    m = x.numel() // k if k else math.prod(x.shape[:-1])
-    if not isinstance(w, torch.Tensor) or w.dim() != 2 or (gated and w.shape[0] % 2):
+    shape = x.shape
+    k = shape[-1]
+    m = shape[0] if len(shape) == 2 else x.numel() // k if k else math.prod(shape[:-1])
+    shape = w.shape if isinstance(w, torch.Tensor) else ()
+    if len(shape) != 2 or (gated and shape[0] % 2):
         raise ValueError("w: a matrix is required, with an even number of rows if the product is gated")
-    if not isinstance(like, torch.Tensor) or like.dtype not in (torch.bfloat16, torch.float16):
+    dt = like.dtype if isinstance(like, torch.Tensor) else None
+    if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError("out, dout: a bfloat16 or float16 tensor is required")
-    rows = w.shape[0]
-    return m, (rows // 2 if gated else rows), k, rows, like.dtype
+    rows = shape[0]
+    return m, (rows // 2 if gated else rows), k, rows, dt
 
 
 def echo_linear8(x, sx, w, sw, out, *, bias=None, residual=None, act="none", gated=False, p=None, workspace=None,

@@ -27,6 +27,7 @@ namespace echo {
 
 struct Tile8Args : TileArgs {
   const float *sx, *sw;
+  int32_t wide;  // rows of scales are whole and aligned groups of four
 };
 
 // X: 0 if x is e4m3, 1 if e5m2 (the instruction's own numbers)

@@ -8,11 +8,12 @@ namespace echo {
 
 constexpr int kC8 = 128;  // contraction length of a step: one block
 
-// Largest first.  As kChunkedCost, measured on this product.
-constexpr TileCost kCost8[kTileKinds] = {{256, 256, 1.45f, 8.5f, 1.45f},
-                                         {256, 128, 0.88f, 4.5f, 0.88f},
-                                         {128, 128, 0.45f, 1.8f, 0.62f},
-                                         {64, 64, 0.185f, 0.8f, 0.22f}};
+// Largest first.  As kChunkedCost, measured on this product (131072 x 1792 and 16384 x
+// 2048 outputs for steps and overheads, 64 to 512 rows of 2048 and 4096 for those alone).
+constexpr TileCost kCost8[kTileKinds] = {{256, 256, 1.75f, 11.0f, 1.75f},
+                                         {256, 128, 1.10f, 5.5f, 1.15f},
+                                         {128, 128, 0.55f, 2.6f, 0.56f},
+                                         {64, 64, 0.27f, 1.0f, 0.27f}};
 
 inline Plan plan_tiles8(int64_t I, int64_t cols, int64_t C) { return plan_by(kCost8, kC8, I, cols, C); }
 

@@ -7,14 +7,25 @@
 namespace echo {
 namespace {
 
-// four bytes per lane from memory into LDS, as dma16 does it with sixteen
-__device__ __forceinline__ void dma4(u32x4 range, lds_short* lds, int offset) {
+// As dma16, with `step` more bytes in a scalar register, and with one word a lane.  (A
+// range is checked with or without `step`: what the calls below mean to be past its end is
+// so by the lane's offset alone.)
+__device__ __forceinline__ void dma16(u32x4 range, lds_short* lds, int offset, int step) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
       "s_nop 4\n\t"
-      "buffer_load_dword %1, %2, 0 offen lds"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
-      : "s"((uint32_t)(uintptr_t)lds), "v"(offset), "s"(range)
+      : "s"((uint32_t)(uintptr_t)lds), "v"(offset), "s"(range), "s"(step)
+      : "memory");
+}
+__device__ __forceinline__ void dma4(u32x4 range, lds_short* lds, int offset, int step) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 4\n\t"
+      "buffer_load_dword %1, %2, %3 offen lds"
+      :
+      : "s"((uint32_t)(uintptr_t)lds), "v"(offset), "s"(range), "s"(step)
       : "memory");
 }
 
@@ -37,28 +48,46 @@ __device__ __forceinline__ u32x4 uniform(u32x4 r) {
 // 32 cycles of the matrix core.
 // Gated, w's tile alternates runs of 32 gate rows and the 32 up rows of the same
 // outputs; a wavefront's loads are of one kind, so each kind has a range of its own.
-template <typename T, int X, int BI, int BJ, int WI, int WJ, bool GATED, int S>
-__global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile8(Tile8Args a) {
-  constexpr int NT = 64 * WI * WJ, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
+// WK sets of wavefronts take the blocks in turn, each with stages and scales of its
+// own, and their sums are added at the end: a small tile's step is bound by the way
+// from the barrier through LDS to its few products, not by their number.
+template <typename T, int X, int BI, int BJ, int WI, int WJ, bool GATED, int S, int WK>
+__global__ __launch_bounds__(64 * WI * WJ * WK, WI * WJ * WK / 4 < 2 ? 2 : WI * WJ * WK / 4) void k_tile8(Tile8Args a) {
+  constexpr int NT = 64 * WI * WJ, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;  // NT, NW: of a set
   constexpr int OUT = GATED ? BJ / 2 : BJ;
   static_assert(!GATED || TJ % 4 == 0, "a gated run is 64 rows of one wavefront");
   static_assert(BI / 64 + 1 <= NW && BJ <= 1024, "a wavefront for each scale load");
   static_assert(128 % (BJ / WJ) == 0, "one block of w to a wavefront's columns");
   constexpr int PA = BI * 8 / NT, PB = BJ * 8 / NT;  // chunks of a thread
-  constexpr int kTileBytes = (BI + BJ) * kC8, kStage = (kTileBytes + NW * 256) / 2;  // in shorts
-  constexpr int kLoads = PA + PB + 1;
-  static_assert((S - 1) * kLoads < 64, "loads in flight");
+  constexpr int kStage = (BI + BJ) * kC8 / 2;  // in shorts
+  constexpr int kLoads = PA + PB;              // and in some steps one of scales
+  static_assert((S - 1) * (kLoads + 1) < 64, "loads in flight");
+  constexpr int kScales = BI / 64 + 1;  // wavefronts that load scales
+  // steps whose scales are there: a group of four is loaded over one that every
+  // wavefront has left behind
+  constexpr int kRing = WK > 1 ? 4 : 8;
+  static_assert(S <= (WK > 1 ? kRing : kRing - 3), "scales in flight");
   constexpr int kEpilogue = kEpilogueFloats<TJ>;
   __shared__ union {
-    short stage[S * kStage];
-    float sums[NW][kEpilogue];
+    struct {
+      short stage[WK][S * kStage];
+      float scales[WK][kRing][kScales * 64];
+    };
+    struct {
+      float sums[NW][kEpilogue];
+      f32x4 others[WK > 1 ? WK - 1 : 1][WK > 1 ? NW : 1][TI * TJ][64];
+    };
   } mem;
-  lds_short* const lds = (lds_short*)mem.stage;
-  typedef __attribute__((address_space(3))) const u32x4 lds_chunk;
   typedef __attribute__((address_space(3))) const float lds_float;
+  typedef __attribute__((address_space(3))) const u32x4 lds_chunk;
 
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, rho = lane & 15;
+  const int lane = threadIdx.x & 63, g = lane >> 4, rho = lane & 15;
+  const int part = WK > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / NW : 0;  // the set
+  const int tid = threadIdx.x - part * NT;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  lds_short* const lds = (lds_short*)mem.stage[part];
+  float* const scales_at = mem.scales[part][0];
+  lds_float* const lds_scales = (lds_float*)scales_at;
   const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
   const uint32_t b = blockIdx.y * gridDim.x + blockIdx.x;
   if (b >= a.workgroups) return;
@@ -66,7 +95,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile8(Tile8Args a) {
   tile_of(b, a.workgroups, a.tiles_i, a.tiles_j, ti, tj, split);
   const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * OUT;
   const int64_t c0 = (int64_t)split * a.chunk, c1 = min(a.C, c0 + a.chunk);
-  const int steps = (int)((c1 - c0 + kC8 - 1) / kC8);
+  const int blocks = (int)((c1 - c0 + kC8 - 1) / kC8), steps = (blocks + WK - 1) / WK;
   const int64_t rows_a = min(a.I - i0, (int64_t)BI), rows_b = min(a.J - j0, (int64_t)OUT);
   const int64_t kb = (a.C + kC8 - 1) / kC8;  // blocks along a row
 
@@ -74,13 +103,21 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile8(Tile8Args a) {
   // move the ranges, in scalar registers.  Every one of a thread's chunks has the
   // same place in its row, and gated its rows of w are 32 apart for each 64.
   const int ca = ((tid & 7) ^ (tid >> 3 & 7)) * 16;
-  const int oa = (int)(tid / 8 * a.lda) + ca;
-  const int ob = (int)((GATED ? tid / 8 & 31 : tid / 8) * a.ldb) + ca;
+  int oa[PA], ob[PB];
+#pragma unroll
+  for (int i = 0; i < PA; ++i) oa[i] = (int)((i * (NT / 8) + tid / 8) * a.lda) + ca;
+#pragma unroll
+  for (int i = 0; i < PB; ++i) {
+    const int r = i * (NT / 8) + tid / 8;
+    ob[i] = (int)((GATED ? (r >> 6) * 32 + (r & 31) : r) * a.ldb) + ca;
+  }
   const char* const pa = (const char*)a.a + i0 * a.lda + c0;
   const char* const pb = (const char*)a.b + j0 * a.ldb + c0;
   // a last chunk's filling is its row's own
   const int64_t whole = (c1 - c0 + 15) & ~(int64_t)15;
   const int64_t end_a = (rows_a - 1) * a.lda + whole, end_b = (rows_b - 1) * a.ldb + whole;
+  const u32x4 ra = uniform(range_of(pa, end_a)), rb = uniform(range_of(pb, end_b));
+  const u32x4 ru = GATED ? uniform(range_of(pb + a.J * a.ldb, end_b)) : rb;
   // the scale that the lane fetches
   int os;
   u32x4 rs;
@@ -98,24 +135,26 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile8(Tile8Args a) {
   rs = uniform(rs);
   constexpr int kPast = 0x7FFFFFF0;  // an offset past every range
 
-  // past the last step nothing is in range, so every step issues as many loads
-  auto stage = [&](lds_short* la, int s) {
+  // The step's block of the set.  Past the last one nothing is in range, so every step
+  // issues as many loads.
+  auto stage = [&](lds_short* la, int step) {
+    const int s = step * WK + part;
     const int64_t left = c1 - c0 - (int64_t)s * kC8;  // of the contraction, from this step on
     const bool past = ca >= left;
-    const int va = past ? kPast : oa, vb = past ? kPast : ob;
-#pragma unroll
-    for (int i = 0; i < PA; ++i) {
-      const int64_t on = i * (NT / 8) * a.lda + s * kC8;
-      dma16(uniform(range_of(pa + on, end_a - on)), la + (i * NT + wave * 64) * 8, va);
+    if (wave < kScales) {
+      if (WK == 1 && a.wide) {
+        if (s % 4 == 0)
+          dma16(rs, (lds_short*)(scales_at + (s % kRing / 4 * kScales + wave) * 256), left <= 0 ? kPast : os, s * 4);
+      } else {
+        dma4(rs, (lds_short*)(scales_at + (step % kRing * kScales + wave) * 64), left <= 0 ? kPast : os, s * 4);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < PA; ++i) dma16(ra, la + (i * NT + wave * 64) * 8, past ? kPast : oa[i], s * kC8);
     lds_short* lb = la + BI * kC8 / 2;
 #pragma unroll
-    for (int i = 0; i < PB; ++i) {
-      const bool up = GATED && ((i * (NT / 8) + wave * 8) >> 5 & 1);
-      const int64_t on = (GATED ? i * (NT / 8) / 64 * 32 : i * (NT / 8)) * a.ldb + s * kC8;
-      dma16(uniform(range_of(pb + on + (up ? a.J * a.ldb : 0), end_b - on)), lb + (i * NT + wave * 64) * 8, vb);
-    }
-    dma4(rs, la + kTileBytes / 2 + wave * 128, left <= 0 ? kPast : os + s * 4);
+    for (int i = 0; i < PB; ++i)
+      dma16(GATED && ((i * (NT / 8) + wave * 8) >> 5 & 1) ? ru : rb, lb + (i * NT + wave * 64) * 8, past ? kPast : ob[i], s * kC8);
   };
 
   // the two chunks of row `row` that the lane holds
@@ -135,85 +174,87 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile8(Tile8Args a) {
   const int odd = (int)((c1 - c0) & 15), last = (int)((c1 - c0) & (kC8 - 1)) >> 4;
   auto cut = [&](lds_short* la) {
     typedef __attribute__((address_space(3))) u32x4 chunk;
-    for (int r = tid; r < BI + BJ; r += NT) {
-      chunk* p = (chunk*)(la + r * (kC8 / 2) + (last ^ (r & 7)) * 8);
-      *p = chunk_before(*p, odd);
+    if ((blocks - 1) % WK == part) {
+      for (int r = tid; r < BI + BJ; r += NT) {
+        chunk* p = (chunk*)(la + r * (kC8 / 2) + (last ^ (r & 7)) * 8);
+        *p = chunk_before(*p, odd);
+      }
     }
     __syncthreads();
   };
 
   // One step's scales, and whether every lane's are powers of two.
   float xs[TI], ws[GATED ? 2 : 1];
-  auto read_scales = [&](const lds_short* la) {
-    lds_float* scales = (lds_float*)(la + kTileBytes / 2);
+  const int wide = WK == 1 && a.wide ? 4 : 1;
+  auto read_scales = [&](int s) {
+    lds_float* scales = lds_scales + (WK == 1 && a.wide ? s % kRing / 4 * kScales * 256 + s % 4 : s % kRing * kScales * 64);
     bool powers = true;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-      xs[i] = scales[wi + i * 16 + rho];
+      xs[i] = scales[(wi + i * 16 + rho) * wide];
       powers = powers && is_power(__float_as_uint(xs[i]));
     }
 #pragma unroll
     for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-      ws[q] = scales[BI + wj / 16 + q * 2];
+      ws[q] = scales[(BI + wj / 16 + q * 2) * wide];
       powers = powers && is_power(__float_as_uint(ws[q]));
     }
     return __builtin_amdgcn_ballot_w64(!powers) == 0;
   };
-  // The step's products, w's fragments read one ahead.  `load` issues the loads of
-  // the step S - 1 ahead behind this step's first reads of LDS.
-  // (The empty assembly keeps a fragment's sums in their place: moved below the
-  // step's other products they would not fit the registers.)
-  auto products = [&](const lds_short* la, auto load, auto pair) {
-    const lds_short* lb = la + BI * kC8 / 2;
-    i32x8 fa[TI], fb[2];
-#pragma unroll
-    for (int i = 0; i < TI; ++i) fa[i] = fragment(la, wi + i * 16 + rho);
-    fb[0] = fragment(lb, wj + rho);
-    load();
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      if (j + 1 < TJ) fb[(j + 1) & 1] = fragment(lb, wj + (j + 1) * 16 + rho);
-#pragma unroll
-      for (int i = 0; i < TI; ++i) pair(fb[j & 1], fa[i], i, j);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  auto arrived = [&](lds_short* la, int s) {
+  // A step begins with its first fragments and the loads of the step S - 1 ahead; its
+  // scales are read behind them, so that nothing waits for their way to the branch
+  // alone.
+  i32x8 fa[TI], fb[2];
+  lds_short *now = lds, *next = lds + (S - 1) * kStage;
+  auto arrive = [&](int s) {
     dma_wait<(S - 2) * kLoads>();
     __syncthreads();
-    if (odd && s == steps - 1) cut(la);
+    if (odd && s == steps - 1) cut(now);
+  };
+  auto read_first = [&] {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) fa[i] = fragment(now, wi + i * 16 + rho);
+    fb[0] = fragment(now + BI * kC8 / 2, wj + rho);
+  };
+  // The step's products, w's fragments read one ahead.
+  auto products = [&](auto pair) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      if (j + 1 < TJ) fb[(j + 1) & 1] = fragment(now + BI * kC8 / 2, wj + (j + 1) * 16 + rho);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) pair(i, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    now = now == lds + (S - 1) * kStage ? lds : now + kStage;
+    next = next == lds + (S - 1) * kStage ? lds : next + kStage;
   };
 
 #pragma unroll
   for (int u = 0; u < S - 1; ++u) stage(lds + u * kStage, u);
-  lds_short *now = lds, *next = lds + (S - 1) * kStage;
-  auto turn = [&] {
-    now = now == lds + (S - 1) * kStage ? lds : now + kStage;
-    next = next == lds + (S - 1) * kStage ? lds : next + kStage;
-  };
   int s = 0;
   bool powers = true;
   for (; s < steps; ++s) {
-    arrived(now, s);
-    powers = read_scales(now);
+    arrive(s);
+    read_first();
+    stage(next, s + S - 1);
+    powers = read_scales(s);
     if (!powers) break;
     int ex[TI], ew[GATED ? 2 : 1];
 #pragma unroll
     for (int i = 0; i < TI; ++i) ex[i] = (int)(__float_as_uint(xs[i]) >> 23);
 #pragma unroll
     for (int q = 0; q < (GATED ? 2 : 1); ++q) ew[q] = (int)(__float_as_uint(ws[q]) >> 23);
-    products(now, [&] { stage(next, s + S - 1); }, [&](i32x8 w, i32x8 x, int i, int j) {
-      acc[i][j] = mfma8<X>(w, x, acc[i][j], ew[GATED ? j >> 1 & 1 : 0], ex[i]);
-    });
-    turn();
+    products([&](int i, int j) { acc[i][j] = mfma8<X>(fb[j & 1], fa[i], acc[i][j], ew[GATED ? j >> 1 & 1 : 0], ex[i]); });
   }
-  // from the first step with another scale on (a wavefront of its own accord: both
-  // loops have the same barriers)
+  // From the first step with another scale on (a wavefront of its own accord: both loops
+  // have the same barriers).  A fragment's products are added while the next one's are
+  // made; the empty assembly keeps that place: moved below the step's other products they
+  // would not fit the registers.
   for (; s < steps; ++s) {
-    if (powers) {
-      arrived(now, s);
-      read_scales(now);
-    }
+    if (powers) arrive(s);
+    read_first();
+    if (powers) stage(next, s + S - 1);
+    read_scales(s);
     powers = true;
     f32x4 t[2][TI];
     auto add = [&](int j) {
@@ -225,40 +266,64 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile8(Tile8Args a) {
         asm volatile("" : "+v"(acc[i][j]));
       }
     };
-    products(now, [&] { stage(next, s + S - 1); }, [&](i32x8 w, i32x8 x, int i, int j) {
-      t[j & 1][i] = mfma8<X>(w, x, f32x4{0.f, 0.f, 0.f, 0.f});
+    products([&](int i, int j) {
+      t[j & 1][i] = mfma8<X>(fb[j & 1], fa[i], f32x4{0.f, 0.f, 0.f, 0.f});
       if (i == TI - 1 && j > 0) add(j - 1);
     });
     add(TJ - 1);
-    turn();
   }
   // nothing may arrive in LDS that the epilogue uses, or after the workgroup has left it
   dma_wait<0>();
   __syncthreads();
+  if constexpr (WK > 1) {
+    f32x4* const mine = mem.others[part > 0 ? part - 1 : 0][wave][0] + lane;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        if (part > 0) mine[(i * TJ + j) * 64] = acc[i][j];
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int p = 0; p < WK - 1; ++p)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] += mem.others[p][wave][i * TJ + j][lane];
+  }
   write_tile<T, GATED, TI, TJ>(a, acc, mem.sums[wave], i0 + wi, j0 + (GATED ? wj / 2 : wj), split, lane);
 }
 
-template <typename T, int X, int BI, int BJ, int WI, int WJ, bool GATED, int S>
+template <typename T, int X, int BI, int BJ, int WI, int WJ, bool GATED, int S, int WK = 1>
 int launch_tile8(Tile8Args a, hipStream_t s) {
   const int64_t out = GATED ? BJ / 2 : BJ;
   const int64_t ti = (a.I + BI - 1) / BI, tj = (a.J + out - 1) / out;
-  constexpr int NT = 64 * WI * WJ;
+  constexpr int NT = 64 * WI * WJ * WK;
   if (ti * tj == 0) return ECHO_SUCCESS;
   a.tiles_i = (uint32_t)ti;
   a.tiles_j = (uint32_t)tj;
   a.workgroups = a.tiles_i * a.tiles_j * a.splits;  // below 2^32 by ECHO_MAX_PRODUCT
   const TileGrid g = grid_of(a.workgroups, NT);
-  return launch(k_tile8<T, X, BI, BJ, WI, WJ, GATED, S>, dim3(g.x, g.y), dim3(NT), s, a);
+  return launch(k_tile8<T, X, BI, BJ, WI, WJ, GATED, S, WK>, dim3(g.x, g.y), dim3(NT), s, a);
 }
 
+// Where a tile's workgroups are no more than the compute units, one has a unit to itself
+// and room for more sets of wavefronts.
 template <typename T, int X, bool GATED>
 int forward8(const Tile8Args& a, int tile, hipStream_t s) {
   constexpr int SI = GATED ? 4 : 2, SJ = GATED ? 1 : 2;  // a gated run is 64 rows of w, in one wavefront
+  const TileCost& k = kCost8[tile];
+  const int64_t cols = GATED ? 2 * a.J : a.J;
+  const bool alone = ((a.I + k.bi - 1) / k.bi) * ((cols + k.bj - 1) / k.bj) * a.splits <= 256;
   switch (tile) {
     case kTile256: return launch_tile8<T, X, 256, 256, 4, 2, GATED, 2>(a, s);
     case kTile256x128: return launch_tile8<T, X, 256, 128, 4, 2, GATED, 3>(a, s);
-    case kTile128: return launch_tile8<T, X, 128, 128, 2, 2, GATED, 2>(a, s);
-    default: return launch_tile8<T, X, 64, 64, SI, SJ, GATED, 4>(a, s);
+    case kTile128:
+      if (alone) return launch_tile8<T, X, 128, 128, 2, 2, GATED, 2, 2>(a, s);
+      return launch_tile8<T, X, 128, 128, 2, 2, GATED, 2>(a, s);
+    default:
+      if (alone) return launch_tile8<T, X, 64, 64, SI, SJ, GATED, 2, 4>(a, s);
+      return launch_tile8<T, X, 64, 64, SI, SJ, GATED, 4>(a, s);
   }
 }
 
