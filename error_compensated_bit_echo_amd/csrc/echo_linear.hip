@@ -13,6 +13,7 @@
 #include "linear_device.h"
 #include "linear_join.h"
 #include "linear_tile.h"
+#include "unpack8_device.h"
 
 using namespace echo;
 
@@ -48,11 +49,11 @@ struct SlopeArgs {
 // P8: p is e4m3 codes with a scale for each 128, gated of two parts; eight codes are
 // read as they lie, since a row's pitch holds its length rounded up to 16.
 template <typename T, bool GATED, bool WHOLE, bool P8>
-__global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
+__device__ __forceinline__ void slope(const SlopeArgs& a, uint32_t bx, uint32_t by) {
   __shared__ float lds[GATED ? 2 : 1][256 * 8 + 32 * 8];
   const int tx = threadIdx.x & (a.wide - 1), ty = threadIdx.x / a.wide, high = 256 / a.wide;
-  const int64_t col = ((int64_t)blockIdx.x * a.wide + tx) * 8;
-  const int64_t r0 = (int64_t)blockIdx.y * a.run, r1 = min(r0 + a.run, a.m);
+  const int64_t col = ((int64_t)bx * a.wide + tx) * 8;
+  const int64_t r0 = (int64_t)by * a.run, r1 = min(r0 + a.run, a.m);
   const int n = (int)min(a.n - col, (int64_t)9);  // 8 or less: the row's last vector
   const int64_t cols = GATED ? 2 * a.n : a.n;
   float sg[8], su[8];
@@ -158,14 +159,41 @@ __global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
     if constexpr (GATED) lds[1][ty * pitch + tx * 8 + e] = su[e];
   }
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * a.wide * 8 + threadIdx.x;
+  const int64_t c = (int64_t)bx * a.wide * 8 + threadIdx.x;
   if ((int)threadIdx.x < a.wide * 8 && c < a.n)
 #pragma unroll
     for (int h = 0; h < (GATED ? 2 : 1); ++h) {
       float s = lds[h][threadIdx.x];
       for (int k = 1; k < high; ++k) s += lds[h][k * pitch + threadIdx.x];
-      a.part[(int64_t)blockIdx.y * cols + h * a.n + c] = s;
+      a.part[(int64_t)by * cols + h * a.n + c] = s;
     }
+}
+
+template <typename T, bool GATED, bool WHOLE>
+__global__ __launch_bounds__(256) void k_slope(SlopeArgs a) {
+  slope<T, GATED, WHOLE, false>(a, blockIdx.x, blockIdx.y);
+}
+
+// From checkpoints in 8 bits, and x unpacked beside it for the product that reads it: one
+// launch less, and the short pass under the long one (32768 x 384 gated and x of 1024:
+// 24 + 17 us one after the other).
+struct Slope8Args {
+  SlopeArgs a;
+  Unpack8Args u;
+  uint32_t across, slopes, unpacks;  // workgroups of a strip of rows, of dp and of x
+  int32_t format;
+};
+
+template <typename T, bool GATED, bool WHOLE>
+__global__ __launch_bounds__(256) void k_slope8(Slope8Args s) {
+  if (blockIdx.x < s.slopes) return slope<T, GATED, WHOLE, true>(s.a, blockIdx.x % s.across, blockIdx.x / s.across);
+  const uint32_t b = blockIdx.x - s.slopes;
+  if (s.format == ECHO_E4M3) {
+    if (s.u.cols % 512 == 0 && s.u.fill == s.u.cols) unpack8<T, ECHO_E4M3, true>(s.u, b, s.unpacks);
+    else unpack8<T, ECHO_E4M3, false>(s.u, b, s.unpacks);
+  } else {
+    unpack8<T, ECHO_E5M2, false>(s.u, b, s.unpacks);
+  }
 }
 
 // ---- rows of odd lengths ------------------------------------------------------------
@@ -305,12 +333,18 @@ int64_t forward_bytes(const Geometry& g) {
 }
 
 template <typename T, bool GATED>
-int run_slope(const SlopeArgs& a, dim3 grid, dim3 block, hipStream_t s) {
-  if (a.sp)
-    return a.n % 8 ? launch(k_slope<T, GATED, false, true>, grid, block, s, a)
-                   : launch(k_slope<T, GATED, true, true>, grid, block, s, a);
-  return a.n % 8 ? launch(k_slope<T, GATED, false, false>, grid, block, s, a)
-                 : launch(k_slope<T, GATED, true, false>, grid, block, s, a);
+int run_slope(const SlopeArgs& a, const Unpack8Args* u, int32_t format, hipStream_t s) {
+  const dim3 grid((uint32_t)((a.n + a.wide * 8 - 1) / (a.wide * 8)), (uint32_t)((a.m + a.run - 1) / a.run)), block(256);
+  if (a.sp) {
+    Slope8Args b = {a, {}, grid.x, grid.x * grid.y, 0, format};
+    if (u) {
+      b.u = *u;
+      b.unpacks = min(unpack_blocks(*u), kMaxBlocks - b.slopes);
+    }
+    const dim3 both(b.slopes + b.unpacks);
+    return a.n % 8 ? launch(k_slope8<T, GATED, false>, both, block, s, b) : launch(k_slope8<T, GATED, true>, both, block, s, b);
+  }
+  return a.n % 8 ? launch(k_slope<T, GATED, false>, grid, block, s, a) : launch(k_slope<T, GATED, true>, grid, block, s, a);
 }
 
 void apply(const Plan& p, void* part, TileArgs& a) {
@@ -388,6 +422,10 @@ int run_backward(How how, const Geometry& g, const BackPlan& b, const void* dout
   // (a gated call without rows has a dp of no bytes too, twice as wide as dout)
   const bool own_dp = b.ld_dp > 0;
   const bool want_dp = own_dp && (dx || dw);
+  Unpack8Args x8 = {};
+  const bool unpack = some && eight && dw && g.k > 0, with_slope = unpack && from.sp;
+  if (unpack) x8 = unpack_args(x, g.ld_x, sx, g.m, g.k, px, round_up(g.k, 8));
+  const Unpack8Args* const unpacked = with_slope ? &x8 : nullptr;
   if (some && (want_dp || dbias)) {
     SlopeArgs a = from;
     a.dout = dout;
@@ -401,11 +439,10 @@ int run_backward(How how, const Geometry& g, const BackPlan& b, const void* dout
     a.act = how.act;
     a.gated = how.gated;
     a.wide = b.wide;
-    const dim3 grid((uint32_t)((g.n + b.wide * 8 - 1) / (b.wide * 8)), (uint32_t)b.runs), block(256);
     if (how.gated)
-      rc = bf16 ? run_slope<bf16_t, true>(a, grid, block, s) : run_slope<f16_t, true>(a, grid, block, s);
+      rc = bf16 ? run_slope<bf16_t, true>(a, unpacked, how.x_format, s) : run_slope<f16_t, true>(a, unpacked, how.x_format, s);
     else
-      rc = bf16 ? run_slope<bf16_t, false>(a, grid, block, s) : run_slope<f16_t, false>(a, grid, block, s);
+      rc = bf16 ? run_slope<bf16_t, false>(a, unpacked, how.x_format, s) : run_slope<f16_t, false>(a, unpacked, how.x_format, s);
     if (rc) return rc;
   }
   if (dbias && g.rows > 0) {
@@ -419,7 +456,7 @@ int run_backward(How how, const Geometry& g, const BackPlan& b, const void* dout
   a.lda = own_dp ? b.ld_dp : g.ld_out;
   a.padded = own_dp;
   void* const splits = (char*)part + b.bias_bytes;
-  if (some && eight && dw) {
+  if (unpack && !with_slope) {
     rc = unpack_rows(x, g.ld_x, sx, how.x_format, g.m, g.k, px, round_up(g.k, 8), how.dtype, s);
     if (rc) return rc;
   }
