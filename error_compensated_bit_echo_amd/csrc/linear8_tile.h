@@ -317,7 +317,6 @@ int forward8(const Tile8Args& a, int tile, hipStream_t s) {
   const bool alone = ((a.I + k.bi - 1) / k.bi) * ((cols + k.bj - 1) / k.bj) * a.splits <= 256;
   switch (tile) {
     case kTile256: return launch_tile8<T, X, 256, 256, 4, 2, GATED, 2>(a, s);
-    case kTile256x128: return launch_tile8<T, X, 256, 128, 4, 2, GATED, 3>(a, s);
     case kTile128:
       if (alone) return launch_tile8<T, X, 128, 128, 2, 2, GATED, 2, 2>(a, s);
       return launch_tile8<T, X, 128, 128, 2, 2, GATED, 2>(a, s);
