@@ -13,6 +13,10 @@ Each rank holds a slice of the block's weights.  Forward, per layer and rank:
 Backward, per layer and rank: echo_linear_backward of both products, the
 all-reduce of the gradient of z, and echo_norm_backward.
 
+With --eight-bit the products read 8-bit floating point (echo_pack8, echo_linear8),
+and z, p and a are kept for the backward pass in 8 bits only
+(echo_linear_backward8), less than half of their bytes.
+
     python examples/tp_layer.py --tokens 1024 --hidden 4096 --inner 1792 --ranks 8
 """
 import argparse
@@ -99,14 +103,9 @@ class Layer:
         self.dnorm = torch.empty_like(self.norm)
         dz = [torch.empty_like(dy) for _ in range(self.ranks)]
         da = empty(tokens, self.inner)
-        need = max(echo.echo_linear_backward_workspace(tokens, hidden, self.inner),
-                   echo.echo_linear_backward_workspace(tokens, self.inner, hidden, act="silu", gated=True),
-                   echo.echo_norm_backward_workspace(tokens, hidden))
+        need = max(self.products_workspace(tokens, hidden), echo.echo_norm_backward_workspace(tokens, hidden))
         ws = empty(need, dtype=torch.uint8)
-        for r in range(self.ranks):
-            echo.echo_linear_backward(dy, self.a[r], self.down[r], None, da, self.ddown[r], workspace=ws)
-            echo.echo_linear_backward(da, self.z, self.up[r], self.p[r], dz[r], self.dup[r], act="silu", gated=True,
-                                      workspace=ws)
+        self.products_backward(dy, da, dz, ws)
         total = torch.empty_like(dy)
         reduce(dz, total)
         out_h, out_y = torch.empty_like(dh), torch.empty_like(dy)
@@ -114,14 +113,75 @@ class Layer:
                                 dw_pre=self.dnorm, workspace=ws)
         return out_h, out_y
 
+    def products_backward(self, dy, da, dz, ws):
+        """every rank's dz and weight gradients; da is one rank's at a time"""
+        for r in range(self.ranks):
+            echo.echo_linear_backward(dy, self.a[r], self.down[r], None, da, self.ddown[r], workspace=ws)
+            echo.echo_linear_backward(da, self.z, self.up[r], self.p[r], dz[r], self.dup[r], act="silu", gated=True,
+                                      workspace=ws)
 
-def run(tokens, hidden, inner, ranks, layers=2, steps=1, seed=0):
+    def products_workspace(self, tokens, hidden):
+        return max(echo.echo_linear_backward_workspace(tokens, hidden, self.inner),
+                   echo.echo_linear_backward_workspace(tokens, self.inner, hidden, act="silu", gated=True))
+
+
+class Layer8(Layer):
+    """The same block with its products in 8-bit floating point, and 8-bit checkpoints."""
+
+    def __init__(self, tokens, hidden, inner, ranks, seed):
+        super().__init__(tokens, hidden, inner, ranks, seed)
+        self.up8 = [self.pack(w, blocks=True, parts=2) for w in self.up]
+        self.down8 = [self.pack(w, blocks=True) for w in self.down]
+        self.z8 = self.space_for(self.z)
+        self.p, self.a = empty(tokens, 2 * inner), empty(tokens, inner)  # of one rank at a time
+        self.p8 = [self.space_for(self.p, parts=2) for _ in range(ranks)]
+        self.a8 = [self.space_for(self.a) for _ in range(ranks)]
+        self.ws_up = empty(echo.echo_linear8_workspace(tokens, inner, hidden, act="silu", gated=True), dtype=torch.uint8)
+        self.ws_down = empty(echo.echo_linear8_workspace(tokens, hidden, inner), dtype=torch.uint8)
+
+    @staticmethod
+    def space_for(x, **how):
+        """codes and scales of a tensor like x"""
+        return echo.codes8_empty(*x.shape), empty(*echo.scales8_shape(*x.shape, **how), dtype=torch.float32)
+
+    def pack(self, x, **how):
+        kept = self.space_for(x, **how)
+        echo.echo_pack8(x, *kept, **how)
+        return kept
+
+    def forward(self, h, y, reduce):
+        if y is None:
+            self.h.copy_(h)
+            echo.echo_norm(h, None, None, self.z, pre="rms", w_pre=self.norm, stats=self.stats)
+        else:
+            echo.echo_norm(h, y, self.h, self.z, pre="rms", w_pre=self.norm, stats=self.stats)
+        echo.echo_pack8(self.z, *self.z8)
+        for r in range(self.ranks):
+            echo.echo_linear8(*self.z8, *self.up8[r], self.a, act="silu", gated=True, p=self.p, workspace=self.ws_up)
+            echo.echo_pack8(self.p, *self.p8[r], parts=2)
+            echo.echo_pack8(self.a, *self.a8[r])
+            echo.echo_linear8(*self.a8[r], *self.down8[r], self.x[r], workspace=self.ws_down)
+        reduce(self.x, self.y)
+        return self.h, self.y
+
+    def products_backward(self, dy, da, dz, ws):
+        for r in range(self.ranks):
+            echo.echo_linear_backward8(dy, *self.a8[r], self.down[r], None, None, da, self.ddown[r], workspace=ws)
+            echo.echo_linear_backward8(da, *self.z8, self.up[r], *self.p8[r], dz[r], self.dup[r], act="silu", gated=True,
+                                       workspace=ws)
+
+    def products_workspace(self, tokens, hidden):
+        return max(echo.echo_linear_backward8_workspace(tokens, hidden, self.inner),
+                   echo.echo_linear_backward8_workspace(tokens, self.inner, hidden, act="silu", gated=True))
+
+
+def run(tokens, hidden, inner, ranks, layers=2, steps=1, seed=0, kind=Layer):
     """`steps` forward and backward passes of a few layers; returns the layers
     and the last step's tensors"""
     gen = torch.Generator(device=DEV).manual_seed(seed)
     h0 = torch.randn(tokens, hidden, generator=gen, device=DEV).to(BF16)
     grad = (1e-3 * torch.randn(tokens, hidden, generator=gen, device=DEV)).to(BF16)
-    blocks = [Layer(tokens, hidden, inner, ranks, seed + 1 + k) for k in range(layers)]
+    blocks = [kind(tokens, hidden, inner, ranks, seed + 1 + k) for k in range(layers)]
     # one call sequence each way: the averages are carried from layer to layer
     there, back = AllReduce(tokens * hidden, ranks), AllReduce(tokens * hidden, ranks)
     for _ in range(steps):
@@ -142,12 +202,14 @@ def main():
     ap.add_argument("--inner", type=int, default=1792, help="columns of the inner product on one rank")
     ap.add_argument("--ranks", type=int, default=8)
     ap.add_argument("--layers", type=int, default=2)
+    ap.add_argument("--eight-bit", action="store_true", help="products and checkpoints in 8-bit floating point")
     args = ap.parse_args()
-    run(args.tokens, args.hidden, args.inner, args.ranks, args.layers)
+    kind = Layer8 if args.eight_bit else Layer
+    run(args.tokens, args.hidden, args.inner, args.ranks, args.layers, kind=kind)
     torch.cuda.synchronize()
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     begin.record()
-    _, out = run(args.tokens, args.hidden, args.inner, args.ranks, args.layers)
+    _, out = run(args.tokens, args.hidden, args.inner, args.ranks, args.layers, kind=kind)
     end.record()
     torch.cuda.synchronize()
     print(f"{args.layers} layers, {args.tokens} tokens x {args.hidden}, {args.ranks} ranks of {args.inner} on one GPU: "
