@@ -3,29 +3,32 @@
 //
 // As in linear_rows.hip: every weight is read once, straight into registers, and
 // meets at most 16 rows, so the call is bound by reading w from HBM, and by latency
-// where w is small.  KW wavefronts share 16 rows of w (gated, the gate and up rows of
-// 8 outputs), deal the contraction's blocks of 128 among them, and add their sums of
-// an output through LDS in a fixed order: eight, or fewer where w has rows enough to
-// fill the compute units with wavefronts that work longer.  Lane 16 g + rho holds
-// bytes 16 g .. + 15 of both halves of a block of row rho, of w and of x, so a load takes
-// 64 neighbours of each row.
+// where w is small.  A workgroup's eight wavefronts share 16 rows of w (gated, the gate
+// and up rows of 8 outputs), deal the contraction's blocks of 128 among them, and add
+// their sums of an output through LDS in a fixed order.  Lane 16 g + rho holds bytes
+// 16 g .. + 15 of both halves of a block of row rho, of w and of x, so a load takes 64
+// neighbours of each row.
+// One row of x, weights from HBM: 32768 x 4096 in 28.8 us (4.7 TB/s), 8192 x 8192 in 16.4
+// (4.1), 4096 x 4096 in 6.1, 4096 x 1792 in 4.2, 1792 x 4096 gated in 5.9; 16 rows 1 to 7 us
+// more, for x, which every workgroup reads from the second-level cache.  What bounds the
+// small ones is one wavefront's way through its loads; 16 wavefronts took 16.6 us for 8192
+// x 8192 and 5.8 for 4096 x 4096, but 15.3 for 9.6 of 32768 x 1024.  Loads that leave the
+// weights out of the caches took 17.2 us where w fits them (8192 x 8192), these 13.2.
 #include "linear8_device.h"
 
 namespace echo {
 namespace {
 
-constexpr int kWaves8 = 8;
+constexpr int KW = 8;  // wavefronts
 
 // U: blocks that are fetched together
-template <typename T, int X, int U, int KW, bool GATED>
-__global__ __launch_bounds__(64 * kWaves8, 4) void k_rows8(Tile8Args a) {
+template <typename T, int X, int U, bool GATED>
+__global__ __launch_bounds__(64 * KW, 4) void k_rows8(Tile8Args a) {
   constexpr int OUT = GATED ? 8 : 16;
-  __shared__ f32x4 lds[kWaves8][64];
+  __shared__ f32x4 lds[KW][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, rho = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int own = wave / KW, turn = wave % KW;
-  const int64_t j0 = ((int64_t)blockIdx.x * (kWaves8 / KW) + own) * OUT;
-  // (a workgroup's last wavefronts may have no rows: they repeat the last ones too)
+  const int turn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t j0 = (int64_t)blockIdx.x * OUT;
   const int64_t kb = (a.C + kC8 - 1) / kC8, down = (a.J + ECHO_FP8_BLOCK - 1) / ECHO_FP8_BLOCK;
   // rows past the end repeat the last one; their sums are not written
   const int64_t wrow = min(j0 + rho % OUT, a.J - 1) + (rho < OUT ? 0 : a.J);
@@ -34,7 +37,7 @@ __global__ __launch_bounds__(64 * kWaves8, 4) void k_rows8(Tile8Args a) {
   const uint8_t* const x = (const uint8_t*)a.a + xrow * a.lda + g * 16;
   const float* const sx = a.sx + xrow * kb;
   // the lane's sums are of rows 4 g .. + 3 of w: gated, gate rows or up rows
-  const float* const sw = a.sw + (min(j0, a.J - 1) / ECHO_FP8_BLOCK + (GATED && g >= 2 ? down : 0)) * kb;
+  const float* const sw = a.sw + (j0 / ECHO_FP8_BLOCK + (GATED && g >= 2 ? down : 0)) * kb;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   auto add = [&](i32x8 fw, i32x8 fx, float s) {
     const f32x4 t = mfma8<X>(fw, fx, f32x4{0.f, 0.f, 0.f, 0.f});
@@ -92,43 +95,37 @@ __global__ __launch_bounds__(64 * kWaves8, 4) void k_rows8(Tile8Args a) {
     }
     add(join16(cw[0], cw[1]), join16(cx[0], cx[1]), sx[full] * sw[full]);
   }
-  lds[wave][lane] = acc;
+  lds[turn][lane] = acc;
   __syncthreads();
   // the first of them finishes: a lane has four rows of w for one of x; gated,
   // the up rows are 32 lanes after their gate's
   const int64_t col = j0 + g * 4;
   if (turn > 0 || lane >= OUT * 4 || rho >= a.I || col >= a.J) return;
   float v[4], u[4];
-  f32x4 sum = lds[wave][lane];
+  f32x4 sum = lds[0][lane];
 #pragma unroll
-  for (int k = 1; k < KW; ++k) sum += lds[wave + k][lane];
+  for (int k = 1; k < KW; ++k) sum += lds[k][lane];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = sum[e];
   if constexpr (GATED) {
-    sum = lds[wave][lane + 32];
+    sum = lds[0][lane + 32];
 #pragma unroll
-    for (int k = 1; k < KW; ++k) sum += lds[wave + k][lane + 32];
+    for (int k = 1; k < KW; ++k) sum += lds[k][lane + 32];
 #pragma unroll
     for (int e = 0; e < 4; ++e) u[e] = sum[e];
   }
   finish<T, 4, GATED>(a, rho, col, (int)min(a.J - col, (int64_t)4), v, u);
 }
 
-template <typename T, int X, int KW, bool GATED>
-int launch_rows(const Tile8Args& a, hipStream_t s) {
-  const int64_t out = (GATED ? 8 : 16) * (kWaves8 / KW);
-  const dim3 grid((uint32_t)((a.J + out - 1) / out)), block(64 * kWaves8);
-  return launch(k_rows8<T, X, 2, KW, GATED>, grid, block, s, a);
-}
-
-// Four wavefronts to sixteen rows where the contraction has no two blocks for eight and
-// w's rows are many (32768 x 1024: 10.4 us against 15.8), else eight (8192 x 8192: 17.2
-// us against 17.8, 4096 x 4096 7.6 against 12.3).
+// Two blocks a wavefront fetches together where it has four or more, else one: 32768 x
+// 1024 9.7 us with one and 15.6 with two, 16384 x 2048 8.7 and 10.1, 4096 x 4096 6.4 and
+// 6.1, 8192 x 4096 9.9 and 9.2.
 template <typename T, int X, bool GATED>
 int rows(const Tile8Args& a, hipStream_t s) {
-  const int64_t groups = (a.J + (GATED ? 7 : 15)) / (GATED ? 8 : 16);
-  if (groups >= 1024 && a.C <= 8 * kC8) return launch_rows<T, X, 4, GATED>(a, s);
-  return launch_rows<T, X, 8, GATED>(a, s);
+  constexpr int kOut = GATED ? 8 : 16;
+  const dim3 grid((uint32_t)((a.J + kOut - 1) / kOut)), block(64 * KW);
+  if (a.C <= 2 * KW * kC8) return launch(k_rows8<T, X, 1, GATED>, grid, block, s, a);
+  return launch(k_rows8<T, X, 2, GATED>, grid, block, s, a);
 }
 
 template <typename T, int X>
