@@ -191,7 +191,7 @@ __global__ __launch_bounds__(256) void k_slope8(Slope8Args s) {
   if (s.format == ECHO_E4M3) {
     if (s.u.cols % 512 == 0 && s.u.fill == s.u.cols) unpack8<T, ECHO_E4M3, true>(s.u, b, s.unpacks);
     else unpack8<T, ECHO_E4M3, false>(s.u, b, s.unpacks);
-  } else {
+  } else {  // x in e5m2 is seldom: the general way alone
     unpack8<T, ECHO_E5M2, false>(s.u, b, s.unpacks);
   }
 }
@@ -339,7 +339,7 @@ int run_slope(const SlopeArgs& a, const Unpack8Args* u, int32_t format, hipStrea
     Slope8Args b = {a, {}, grid.x, grid.x * grid.y, 0, format};
     if (u) {
       b.u = *u;
-      b.unpacks = min(unpack_blocks(*u), kMaxBlocks - b.slopes);
+      b.unpacks = min(unpack_blocks(*u), kMaxBlocksHip - b.slopes);  // slopes: some thousand
     }
     const dim3 both(b.slopes + b.unpacks);
     return a.n % 8 ? launch(k_slope8<T, GATED, false>, both, block, s, b) : launch(k_slope8<T, GATED, true>, both, block, s, b);

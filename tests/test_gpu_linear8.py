@@ -99,6 +99,12 @@ def test_few_rows(m, n, k, gated, dt):
     forward(case(m, n, k, dt, gated, fmt="e5m2", scales="any", seed=1), "gelu")
 
 
+@pytest.mark.parametrize("k", [1023, 1920, 2047, 2048, 2049, 2177, 4095, 4097])
+@pytest.mark.parametrize("gated", [False, True])
+def test_few_rows_of_every_share_of_blocks(gated, k):
+    forward(case(11, 40, k, torch.bfloat16, gated, scales="any"), "silu" if gated else "none")
+
+
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("m,n,k", [(17, 16, 128), (64, 64, 128), (65, 63, 127), (63, 65, 129), (128, 128, 256), (129, 200, 384),
@@ -149,6 +155,20 @@ def test_in_place_residual(m):
     B.echo_linear8(c["x"], on(c["sx"]), c["w"], on(c["sw"]), out, bias=on(c["bias"]), residual=out,
                    workspace=space(B.echo_linear8_workspace(m, 64, 256)))
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("m,n,k", [(1000, 520, 96), (4100, 2060, 64)])
+def test_in_place_residual_of_many_tiles(m, n, k):
+    """rows and columns at odd addresses, whose last tiles are cut both ways"""
+    c = case(m, n, k, torch.float16)
+    w, room = (c["w"], on(c["sw"])), space(B.echo_linear8_workspace(m, n, k, act="relu"))
+    want = torch.empty(m, n, dtype=torch.float16, device=DEV)
+    B.echo_linear8(c["x"], on(c["sx"]), *w, want, bias=on(c["bias"]), residual=on(c["residual"]), act="relu", workspace=room)
+    buf, out = guarded(m, n, torch.float16, n + 3, 1)
+    out.copy_(c["residual"])
+    B.echo_linear8(c["x"], on(c["sx"]), *w, out, bias=on(c["bias"]), residual=out, act="relu", workspace=room)
+    assert torch.equal(out, want)
+    untouched(buf, out, "out")
 
 
 @pytest.mark.parametrize("m,n,k", [(0, 8, 8), (4, 0, 8), (4, 8, 0), (40, 8, 0)])
