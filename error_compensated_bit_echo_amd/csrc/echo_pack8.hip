@@ -6,10 +6,13 @@
 // loads and stores are each one run, and sixteen threads have a block's 128 columns,
 // whose largest magnitude comes from four steps over their lanes (DPP).  Two such
 // vectors a thread, both on their way before the first is used, and stores that do not
-// stay in the caches: 8192 x 4096 bf16 packed in 15.3 us and unpacked in 15.1 (6.7
-// TB/s), against 17 to 20 us with one vector, with cached stores or with uncached
-// loads, and 31 us with sixteen neighbours a thread.  Dividing by the scale is a
-// multiplication with its reciprocal, exact for a power of two.
+// stay in the caches: 8192 x 4096 bf16 packed in 16.9 us (6.0 TB/s) and 32768 x 1024
+// unpacked in 16.2 (6.3 TB/s; a large copy reaches 6.5), 17 to 20 us with one vector, with
+// cached stores or with uncached loads, 31 with sixteen neighbours a thread.  256 x 4096
+// takes 3.2 us, which is latency.  Rows are found by a multiplication and, where a
+// wavefront stays in one row, in scalar registers (packed 21.0 -> 18.2 us with its launch,
+// unpacked 23.4 -> 16.7; 4072 x 2051 f16 from e5m2 8.9 -> 7.7).  Dividing by the scale is
+// a multiplication with its reciprocal, exact for a power of two.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -153,6 +156,9 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
 
 // Blocks of 128 x 128, a workgroup each; a thread has eight columns of eight rows in
 // registers, so the transposed codes need no second reading and no LDS.
+// 3584 x 4096 bf16 with its transpose in 14.6 us (4.0 TB/s): 896 workgroups are one round
+// whose loads, block's scale and stores follow each other, and the transposed rows' stores
+// are eight bytes at a time, which the caches join.
 template <typename T, int FORMAT, bool WHOLE, bool TURN>
 __global__ __launch_bounds__(256) void k_pack8_blocks(Pack8Args a) {
   __shared__ uint32_t most[4];

@@ -38,8 +38,11 @@ __device__ __forceinline__ u32x4 uniform(u32x4 r) {
 
 // A wavefront's sums to the epilogue or to a split's partial sums, through LDS as
 // write_tile has them.  A short contraction's time is this one's: the bias is the same for
-// all of a lane's rows and is read once, and the residual of a pass is on its way three
-// passes before it is added (26490 x 480 x 94 with bias, residual and p kept: 35.6 -> 28.5 us).
+// all of a lane's rows and is read once, the residual of a pass is on its way three passes
+// before it is added (two: 5 % more), and the passes are unrolled.  26490 x 480 x 94 with
+// bias, residual and p kept 35.7 -> 26.9 us, 8192 x 4096 x 256 with residual 54.1 -> 45.6,
+// 8192 x 4096 x 1792 94.1 -> 85.3, 131072 x 1792 x 4096 913 -> 905.  With exact GELU's gate
+// (23589 x 2944 x 128: 112 us) it is bound by the activation's arithmetic.
 template <typename T, bool GATED, int TI, int TJ>
 __device__ __forceinline__ void write_tile8(const TileArgs& a, const f32x4 (&acc)[TI][TJ], float* lds, int64_t i0,
                                             int64_t j0, uint32_t split, int lane) {
@@ -87,12 +90,10 @@ __device__ __forceinline__ void write_tile8(const TileArgs& a, const f32x4 (&acc
 #pragma unroll
     for (int j = 0; j < TJ; ++j) *(f32x4*)(lds + rho * kPitch + ((j * 4 + g) ^ (rho & kTurn)) * 4) = acc[i][j];
     __builtin_amdgcn_wave_barrier();
-    float v[8], u[8];
-    read(in_pass, v, u);
-#pragma unroll 1
+#pragma unroll
     for (int r = 0; r < 16; r += kRowsOf) {
-      float nv[8], nu[8];  // the next pass's sums on their way
-      read(min(r + kRowsOf, 16 - kRowsOf) + in_pass, nv, nu);
+      float v[8], u[8];
+      read(r + in_pass, v, u);
       u32x4 next = {};
       if (adds && whole) next = fetch(i * 16 + r + kAhead * kRowsOf);
       const int64_t row = i0 + i * 16 + r + in_pass;
@@ -133,11 +134,6 @@ __device__ __forceinline__ void write_tile8(const TileArgs& a, const f32x4 (&acc
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = nv[e];
-        u[e] = nu[e];
-      }
-#pragma unroll
       for (int p = 0; p + 1 < kAhead; ++p) res[p] = res[p + 1];
       res[kAhead - 1] = next;
     }
@@ -160,6 +156,17 @@ __device__ __forceinline__ void write_tile8(const TileArgs& a, const f32x4 (&acc
 // WK sets of wavefronts take the blocks in turn, each with stages and scales of its
 // own, and their sums are added at the end: a small tile's step is bound by the way
 // from the barrier through LDS to its few products, not by their number.
+//
+// What bounds it: a step of 256 x 256 takes 1.7 us, and 1.14 of them without its loads
+// (products and fragments alone; the matrix cores' own 2048 cycles are .85 at 2.4 GHz):
+// the 64 KB from the second-level cache to LDS, 30 bytes a cycle and compute
+// unit, do not hide whole.  A tile's filling and epilogue are another 11 us, 8 of them
+// stores, which nothing of a lone workgroup covers.  131072 x 1792 x 4096 in 876 to 905 us
+// (2.13 to 2.20 PFLOP/s), 8192 x 1792 x 4096 gated in 124 with powers of two and 132 with
+// other scales, 256 x 4096 x 1792 in 10.5 (64 x 64, four sets).
+// Measured and slower: fragments read across the steps' barrier; four wavefronts of 128 x
+// 128 (1.86 us a step); loads into the second-level cache ahead of the tile's; two stages
+// more for lone small tiles; outputs stored around the caches.
 template <typename T, int X, int BI, int BJ, int WI, int WJ, bool GATED, int S, int WK>
 __global__ __launch_bounds__(64 * WI * WJ * WK, WI * WJ * WK / 4 < 2 ? 2 : WI * WJ * WK / 4) void k_tile8(Tile8Args a) {
   constexpr int NT = 64 * WI * WJ, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;  // NT, NW: of a set
@@ -251,6 +258,8 @@ __global__ __launch_bounds__(64 * WI * WJ * WK, WI * WJ * WK / 4 < 2 ? 2 : WI * 
     const int64_t left = c1 - c0 - (int64_t)s * kC8;  // of the contraction, from this step on
     const bool past = ca >= left;
     if (wave < kScales) {
+      // four steps' scales at once, where their rows begin at 16 bytes (8192 x 4096 x 4096
+      // 139 us, 144 one by one; 32768 rows 539 and 559)
       if (WK == 1 && a.wide) {
         if (s % 4 == 0)
           dma16(rs, (lds_short*)(scales_at + (s % kRing / 4 * kScales + wave) * 256), left <= 0 ? kPast : os, s * 4);
@@ -417,7 +426,9 @@ int launch_tile8(Tile8Args a, hipStream_t s) {
 }
 
 // Where a tile's workgroups are no more than the compute units, one has a unit to itself
-// and room for more sets of wavefronts.
+// and room for more sets of wavefronts (64 x 2048 x 2048 9.7 us, with one set 11.7; 1024 x
+// 1024 x 4096 16.4 and 19.6; 2048 x 2048 x 2048 20.2 and 21.9; 256 x 4096 x 1792 11.5 and
+// 11.7, weights from HBM).
 template <typename T, int X, bool GATED>
 int forward8(const Tile8Args& a, int tile, hipStream_t s) {
   constexpr int SI = GATED ? 4 : 2, SJ = GATED ? 1 : 2;  // a gated run is 64 rows of w, in one wavefront
