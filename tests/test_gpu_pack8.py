@@ -278,3 +278,47 @@ def test_stream_and_graph():
     torch.cuda.synchronize()
     w, s = F.pack(x.cpu().double().numpy(), "e4m3", False, 1)
     same_codes(bytes_of(codes), w, "e4m3", "codes")
+
+
+@pytest.mark.parametrize("cols,blocks", [(33000, False), (33280, False), (33000, True)])
+def test_offsets_past_32_bits(cols, blocks):
+    """a matrix of more than 2^31 elements, its first and last rows looked at: of odd
+    length, of whole wavefronts, and in blocks of 128 x 128 with its transpose"""
+    rows, some = 65664, 128
+    top, end = draw(some, cols, torch.bfloat16, 1), draw(some, cols, torch.bfloat16, 2)
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[:some], x[-some:] = top.to(DEV), end.to(DEV)
+    codes, scales = B.codes8_empty(rows, cols), torch.empty(B.scales8_shape(rows, cols, blocks=blocks), device=DEV)
+    turned = [B.codes8_empty(cols, rows), torch.empty(tuple(scales.shape)[::-1], device=DEV)] if blocks else [None, None]
+    print(f"pack {rows} x {cols} blocks={blocks}", flush=True)
+    B.echo_pack8(x, codes, scales, blocks=blocks, codes_t=turned[0], scales_t=turned[1])
+    back = torch.full_like(x, 1.0)
+    B.echo_unpack8(codes, scales, back, blocks=blocks)
+    torch.cuda.synchronize()
+    high = 1 if blocks else some  # rows of scales
+    for part, sel, ssel in ((top, slice(0, some), slice(0, high)), (end, slice(rows - some, rows), slice(-high, None))):
+        want, ws = F.pack(part.double().numpy(), "e4m3", blocks, 1)
+        same_codes(bytes_of(codes[sel]), want, "e4m3", "codes")
+        np.testing.assert_array_equal(scales[ssel].cpu().double().numpy(), ws)
+        if blocks:
+            same_codes(bytes_of(turned[0].view(torch.uint8)[:, sel]), want.T, "e4m3", "codes_t")
+            np.testing.assert_array_equal(turned[1][:, ssel].cpu().double().numpy(), ws.T)
+        values = torch.from_numpy(F.values(want, ws, "e4m3", blocks)).to(torch.bfloat16)
+        assert torch.equal(back[sel].cpu(), values)
+    assert not back[some:-some].any()
+
+
+def test_more_vectors_than_a_32_bit_division_counts():
+    """2^31 vectors of eight and a few, two to a row"""
+    rows, cols, last = (1 << 30) + 5, 9, 4099
+    codes = torch.zeros(rows, 16, dtype=torch.uint8, device=DEV)
+    raw = torch.randint(0, 120, (last, 16), generator=torch.Generator().manual_seed(3), dtype=torch.uint8)
+    codes[-last:] = raw.to(DEV)
+    scales = torch.ones(rows, 1, device=DEV)
+    scales[-last:, 0] = torch.exp2(torch.arange(last, device=DEV) % 7 - 3.0)
+    x = torch.ones(rows, cols, dtype=torch.float16, device=DEV)
+    B.echo_unpack8(codes[:, :cols].view(torch.float8_e4m3fn), scales, x)
+    torch.cuda.synchronize()
+    want = F.values(raw[:, :cols].numpy(), scales[-last:].cpu().double().numpy(), "e4m3")
+    assert torch.equal(x[-last:].cpu(), torch.from_numpy(want).half())
+    assert not x[:-last].any()
