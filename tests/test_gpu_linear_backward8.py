@@ -190,3 +190,40 @@ def test_streams_and_graph():
             o.zero_()
         graph.replay()
         assert same()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_offsets_past_32_bits(gated):
+    """codes of p past 2^31 bytes, dout and dp past 2^32: the first and last rows have a
+    gradient, and sums over all rows add nothing of the others (a zero rounds nothing, so
+    the bounds are of the rows that have one)"""
+    m, n, k, some = 131200, 8264 if gated else 16520, 16, 96
+    c = case(2 * some, n, k, torch.bfloat16, "relu", gated)
+
+    def grown(t):
+        big = torch.zeros(m, t.shape[1], dtype=t.dtype, device=DEV)
+        big[:some], big[-some:] = t[:some], t[some:]
+        return big
+
+    def codes(t):
+        big = B.codes8_empty(m, t.shape[1])
+        big.view(torch.uint8).zero_()
+        big.view(torch.uint8)[:some], big.view(torch.uint8)[-some:] = t.view(torch.uint8)[:some], t.view(torch.uint8)[some:]
+        return big
+
+    rows = c["w"].shape[0]
+    dx, dw = torch.empty(m, k, dtype=c["dt"], device=DEV), torch.empty(rows, k, dtype=c["dt"], device=DEV)
+    db = torch.empty(rows, dtype=c["dt"], device=DEV)
+    print(f"linear_backward8 m={m} n={n} k={k} gated={gated}", flush=True)
+    B.echo_linear_backward8(grown(on(c["dout"])), codes(c["x"]), grown(on(c["sx"])), on(c["w"]), codes(c["p"]), grown(on(c["sp"])),
+                            dx, dw, dbias=db, act="relu", gated=gated,
+                            workspace=space(B.echo_linear_backward8_workspace(m, n, k, act="relu", gated=gated)))
+    torch.cuda.synchronize()
+    exact = R.linear_backward(c["dout"], torch.from_numpy(c["xv"]), c["w"], torch.from_numpy(c["pv"]), "relu", gated)
+    half = R.HALF_ULP[c["dt"]] / R.EPS32
+    for q, v, length in (("dx", torch.cat([dx[:some], dx[-some:]]), rows), ("dw", dw, 2 * some), ("dbias", db, 2 * some)):
+        e, magnitude = exact[q][:2]
+        if q != "dbias":
+            magnitude = magnitude + 1.01 * half / (length + 64) * exact[q][2]
+        R.close(v, e, magnitude, length + 64, q)
+    assert not dx[some:-some].any()
