@@ -166,7 +166,8 @@ __device__ __forceinline__ void write_tile8(const TileArgs& a, const f32x4 (&acc
 // other scales, 256 x 4096 x 1792 in 10.5 (64 x 64, four sets).
 // Measured and slower: fragments read across the steps' barrier; four wavefronts of 128 x
 // 128 (1.86 us a step); loads into the second-level cache ahead of the tile's; two stages
-// more for lone small tiles; outputs stored around the caches.
+// more for lone small tiles; outputs stored around the caches; workgroups that go on to a
+// next tile with its first loads under the epilogue (2 to 4 % slower).
 template <typename T, int X, int BI, int BJ, int WI, int WJ, bool GATED, int S, int WK>
 __global__ __launch_bounds__(64 * WI * WJ * WK, WI * WJ * WK / 4 < 2 ? 2 : WI * WJ * WK / 4) void k_tile8(Tile8Args a) {
   constexpr int NT = 64 * WI * WJ, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;  // NT, NW: of a set
