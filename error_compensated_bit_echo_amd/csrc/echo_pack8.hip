@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kBlock) void k_pack8_rows(Pack8Args a) {
         clear_from(r[u], n[u]);
       }
       const uint32_t largest = n[u] > 0 ? largest_of_raw(r[u]) : 0;
-      const int e = scale_exponent<FORMAT>(lanes_max<16>(largest));
+      const int e = scale_exponent<FORMAT>(lanes_max(largest));
       const float inverse = power_of_two(254 - e);
       float f[8];
       unpack_raw(r[u], f);
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(256) void k_pack8_blocks(Pack8Args a) {
     for (int r = 0; r < 8; ++r)
 #pragma unroll
       for (int i = 0; i < 8; ++i) largest = max(largest, magnitude(f[r][i]));
-    largest = lanes_max<16>(largest);
+    largest = lanes_max(largest);
     largest = max(max((uint32_t)__builtin_amdgcn_readlane((int)largest, 0), (uint32_t)__builtin_amdgcn_readlane((int)largest, 16)),
                   max((uint32_t)__builtin_amdgcn_readlane((int)largest, 32), (uint32_t)__builtin_amdgcn_readlane((int)largest, 48)));
     __syncthreads();  // the block before has read its four

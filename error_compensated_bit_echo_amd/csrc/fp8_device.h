@@ -13,7 +13,6 @@ namespace echo {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
-typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
 
 // eight codes, in the order of their bytes (v_cvt_pk_fp8_f32, v_cvt_pk_bf8_f32:
 // nearest even; nothing past the largest code comes here but inf and NaN)
@@ -71,8 +70,7 @@ __device__ __forceinline__ int scale_exponent(uint32_t largest) {
 }
 __device__ __forceinline__ float power_of_two(int biased) { return __uint_as_float((uint32_t)biased << 23); }
 
-// largest of LANES = 8 or 16 neighbouring lanes, in all of them
-template <int LANES>
+// largest of sixteen neighbouring lanes, in all of them
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   auto step = [&](auto ctrl) {
     const uint32_t o =
@@ -82,7 +80,7 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   step(std::integral_constant<int, 0xB1>{});   // lane ^ 1
   step(std::integral_constant<int, 0x4E>{});   // lane ^ 2
   step(std::integral_constant<int, 0x141>{});  // row_half_mirror
-  if constexpr (LANES == 16) step(std::integral_constant<int, 0x140>{});  // row_mirror
+  step(std::integral_constant<int, 0x140>{});  // row_mirror
   return v;
 }
 
