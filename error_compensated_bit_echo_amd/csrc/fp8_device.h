@@ -108,23 +108,66 @@ template <typename T, int FORMAT>
 __device__ __forceinline__ bool may_pass(float scale) {
   return fabsf(scale) > largest_of<T>() / (FORMAT == ECHO_E4M3 ? 448.f : 57344.f);
 }
-// a code's value before its rounding to T; finite codes stay finite
+// Code times scale, then rounded to a 16-bit type, is rounded once: binary32 holds the product
+// where a scale has no more than 20 digits, which makes 24 with a code's, and lies above the
+// subnormal numbers; of others a number halfway between two of the type may be one that the
+// product was rounded to.
+__device__ __forceinline__ bool may_lose(float scale) {
+  const uint32_t b = __float_as_uint(scale);
+  return (b & 15) != 0 || ((b & 0x007FFFFFu) != 0 && fabsf(scale) < 0x1p-100f);
+}
+// Whether one of eight may lie halfway between two numbers of T.  Its last 16 bits say so
+// for bfloat16; for half, whose subnormal numbers have their digits further up, the last 12
+// are 0, as they are for 0, which is looked for only then.
 template <typename T>
-__device__ __forceinline__ float value_of(float code, float scale) {
-  const float v = code * scale;
-  return fabsf(v) > largest_of<T>() && fabsf(code) < __builtin_inff() ? copysignf(largest_of<T>(), v) : v;
+__device__ __forceinline__ bool any_halfway(const float (&f)[8]) {
+  constexpr bool kHalf = std::is_same<T, f16_t>::value;
+  uint32_t least = ~0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(f[i]);
+    least = min(least, kHalf ? b << 20 : (b << 16) + 0x80000000u);
+  }
+  if (least > 0 || !kHalf) return least == 0;
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) any |= (__float_as_uint(f[i]) & 0xFFFu) == 0 && f[i] != 0.f;
+  return any;
+}
+// The product rounded to odd: of the two binary32 numbers around one that is neither, that
+// with its last bit set, which lies halfway between no two of a 16-bit type and on the
+// product's side.  `up` lifts products of small scales from below binary32's smallest number.
+// Unpacked with scales of all digits 32768 x 1024 takes 16.5 us (bf16) and 16.2 (f16), as with
+// powers of two; every product to odd took 20.2, its remainder from binary64 23.
+__device__ __forceinline__ float times_to_odd(float code, float scale) {
+  const float v = code * scale, up = fabsf(scale) < 1.f ? 0x1p64f : 1.f;
+  const float rest = fmaf(code, scale * up, -(v * up));
+  const uint32_t b = __float_as_uint(v);
+  const int outwards = (int)(__float_as_uint(rest) ^ b) >> 31 | 1;  // 1: the product is larger
+  return __uint_as_float((b & 1) == 0 && (rest < 0.f || rest > 0.f) ? b + outwards : b);
 }
 
-// eight codes times their scale
+// eight codes times their scale, to be rounded to T; finite codes stay finite
 template <typename T, int FORMAT>
 __device__ __forceinline__ void values_of(u32x2 w, float scale, float (&f)[8]) {
   values_of<FORMAT>(w, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] *= scale;
+  if constexpr (sizeof(T) == 2) {
+    if (may_lose(scale)) {
+      if (any_halfway<T>(f)) {
+        values_of<FORMAT>(w, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = times_to_odd(f[i], scale);
+      }
+    }
+  }
   if (may_pass<T, FORMAT>(scale)) {
+    float c[8];
+    values_of<FORMAT>(w, c);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = value_of<T>(f[i], scale);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= scale;
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(f[i]) > largest_of<T>() && fabsf(c[i]) < __builtin_inff()) f[i] = copysignf(largest_of<T>(), f[i]);
   }
 }
 
