@@ -164,7 +164,10 @@ __device__ __forceinline__ void write_tile8(const TileArgs& a, const f32x4 (&acc
 // stores, which nothing of a lone workgroup covers.  131072 x 1792 x 4096 in 876 to 905 us
 // (2.13 to 2.20 PFLOP/s), 8192 x 1792 x 4096 gated in 124 with powers of two and 132 with
 // other scales, 256 x 4096 x 1792 in 10.5 (64 x 64, four sets).
-// Measured and slower: fragments read across the steps' barrier; four wavefronts of 128 x
+// Measured and slower: a step with scales whose product is below 2^-126 added once more, by
+// one scale after the other (a branch at the end of each step with other scales: 8192 x 1792
+// x 4096 gated 124 -> 128 us, 131072 x 1792 x 4096 985 -> 1005; the header has what such
+// products lose); fragments read across the steps' barrier; four wavefronts of 128 x
 // 128 (1.86 us a step); loads into the second-level cache ahead of the tile's; two stages
 // more for lone small tiles; outputs stored around the caches; workgroups that go on to a
 // next tile with its first loads under the epilogue (2 to 4 % slower).
