@@ -14,8 +14,9 @@ Backward, per layer and rank: echo_linear_backward of both products, the
 all-reduce of the gradient of z, and echo_norm_backward.
 
 With --eight-bit the products read 8-bit floating point (echo_pack8, echo_linear8),
-and z, p and a are kept for the backward pass in 8 bits only
-(echo_linear_backward8), less than half of their bytes.
+and each layer keeps z, p and a for its backward pass in 8 bits only
+(echo_linear_backward8): 33 bytes for 64 of theirs, a byte an element and a scale for
+each 128.  Their 16-bit forms are there once for all layers.
 
     python examples/tp_layer.py --tokens 1024 --hidden 4096 --inner 1792 --ranks 8
 """
@@ -65,21 +66,27 @@ class AllReduce:
 class Layer:
     """One block's weights, dealt to the ranks, and what its backward pass needs."""
 
-    def __init__(self, tokens, hidden, inner, ranks, seed):
+    def __init__(self, tokens, hidden, inner, ranks, seed, beside=None):
+        """`beside`: another layer of the same sizes"""
         gen = torch.Generator(device=DEV).manual_seed(seed)
         draw = lambda *s: (torch.randn(*s, generator=gen, device=DEV) * s[-1] ** -0.5).to(BF16)  # noqa: E731
         self.up = [draw(2 * inner, hidden) for _ in range(ranks)]    # gate rows, then up rows
         self.down = [draw(hidden, inner) for _ in range(ranks)]
         self.norm = torch.ones(hidden, dtype=BF16, device=DEV)
         self.ranks, self.inner = ranks, inner
-        self.h, self.z, self.y = (empty(tokens, hidden) for _ in range(3))
+        self.h, self.y = empty(tokens, hidden), empty(tokens, hidden)
         self.stats = empty(4, tokens, dtype=torch.float32)
-        self.p = [empty(tokens, 2 * inner) for _ in range(ranks)]
-        self.a = [empty(tokens, inner) for _ in range(ranks)]
+        self.kept(tokens, hidden, beside)
         self.x = [empty(tokens, hidden) for _ in range(ranks)]
         space = lambda *a, **k: empty(echo.echo_linear_workspace(*a, **k), dtype=torch.uint8)  # noqa: E731
         self.ws_up = space(tokens, inner, hidden, act="silu", gated=True)
         self.ws_down = space(tokens, hidden, inner)
+
+    def kept(self, tokens, hidden, beside):
+        """what the forward pass keeps of z, p and a"""
+        self.z = empty(tokens, hidden)
+        self.p = [empty(tokens, 2 * self.inner) for _ in range(self.ranks)]
+        self.a = [empty(tokens, self.inner) for _ in range(self.ranks)]
 
     def forward(self, h, y, reduce):
         """h, the stream, and y, the block before's output (None for the first)"""
@@ -128,16 +135,20 @@ class Layer:
 class Layer8(Layer):
     """The same block with its products in 8-bit floating point, and 8-bit checkpoints."""
 
-    def __init__(self, tokens, hidden, inner, ranks, seed):
-        super().__init__(tokens, hidden, inner, ranks, seed)
+    def __init__(self, tokens, hidden, inner, ranks, seed, beside=None):
+        super().__init__(tokens, hidden, inner, ranks, seed, beside)
         self.up8 = [self.pack(w, blocks=True, parts=2) for w in self.up]
         self.down8 = [self.pack(w, blocks=True) for w in self.down]
-        self.z8 = self.space_for(self.z)
-        self.p, self.a = empty(tokens, 2 * inner), empty(tokens, inner)  # of one rank at a time
-        self.p8 = [self.space_for(self.p, parts=2) for _ in range(ranks)]
-        self.a8 = [self.space_for(self.a) for _ in range(ranks)]
         self.ws_up = empty(echo.echo_linear8_workspace(tokens, inner, hidden, act="silu", gated=True), dtype=torch.uint8)
         self.ws_down = empty(echo.echo_linear8_workspace(tokens, hidden, inner), dtype=torch.uint8)
+
+    def kept(self, tokens, hidden, beside):
+        # z, and p and a of one rank at a time, are packed as soon as they are there
+        self.z, self.p, self.a = (beside.z, beside.p, beside.a) if beside else (
+            empty(tokens, hidden), empty(tokens, 2 * self.inner), empty(tokens, self.inner))
+        self.z8 = self.space_for(self.z)
+        self.p8 = [self.space_for(self.p, parts=2) for _ in range(self.ranks)]
+        self.a8 = [self.space_for(self.a) for _ in range(self.ranks)]
 
     @staticmethod
     def space_for(x, **how):
@@ -181,7 +192,9 @@ def run(tokens, hidden, inner, ranks, layers=2, steps=1, seed=0, kind=Layer):
     gen = torch.Generator(device=DEV).manual_seed(seed)
     h0 = torch.randn(tokens, hidden, generator=gen, device=DEV).to(BF16)
     grad = (1e-3 * torch.randn(tokens, hidden, generator=gen, device=DEV)).to(BF16)
-    blocks = [kind(tokens, hidden, inner, ranks, seed + 1 + k) for k in range(layers)]
+    blocks = []
+    for k in range(layers):
+        blocks.append(kind(tokens, hidden, inner, ranks, seed + 1 + k, beside=blocks[0] if blocks else None))
     # one call sequence each way: the averages are carried from layer to layer
     there, back = AllReduce(tokens * hidden, ranks), AllReduce(tokens * hidden, ranks)
     for _ in range(steps):
