@@ -86,7 +86,7 @@ int echo_linear8(const echo_linear8_desc* d, const void* x, const float* sx, con
   a.splits = (uint32_t)plan.splits;
   a.chunk = plan.chunk;
   a.part = plan.splits > 1 ? (float*)workspace : nullptr;
-  a.wide = blocks_of(g.k) % 4 == 0 && plan.chunk / kC8 % 4 == 0 && aligned(sx, 16) && aligned(sw, 16);
+  a.wide = scales_in_fours(plan, g.k) && aligned(sx, 16) && aligned(sw, 16);
   rc = d->x_format == ECHO_E4M3 ? tile8_e4m3(a, d->dtype, gated, plan.tile, s)
                                 : tile8_e5m2(a, d->dtype, gated, plan.tile, s);
   if (rc || plan.splits == 1) return rc;

@@ -16,6 +16,12 @@ constexpr TileCost kCost8[kTileKinds] = {{256, 256, 1.75f, 11.0f, 1.75f},
                                          {128, 128, 0.55f, 2.6f, 0.56f},
                                          {64, 64, 0.27f, 1.0f, 0.27f}};
 
+// Whether every row of scales, and every split's part of it, is whole groups of four: four
+// steps' scales are then loaded at once (if the scales are aligned, too).
+inline bool scales_in_fours(const Plan& p, int64_t C) {
+  return (C + kC8 - 1) / kC8 % 4 == 0 && p.chunk / kC8 % 4 == 0;
+}
+
 inline Plan plan_tiles8(int64_t I, int64_t cols, int64_t C) { return plan_by(kCost8, kC8, I, cols, C); }
 
 }  // namespace echo
