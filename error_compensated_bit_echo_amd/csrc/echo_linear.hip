@@ -191,7 +191,9 @@ __global__ __launch_bounds__(256) void k_slope8(Slope8Args s) {
   if (s.format == ECHO_E4M3) {
     if (s.u.cols % 512 == 0 && s.u.fill == s.u.cols) unpack8<T, ECHO_E4M3, true>(s.u, b, s.unpacks);
     else unpack8<T, ECHO_E4M3, false>(s.u, b, s.unpacks);
-  } else {  // x in e5m2 is seldom: the general way alone
+  } else {
+    // in the general way alone: the whole call takes the same with x in either format (32768 x
+    // 384 x 1024 gated 156 to 159 us, 8192 x 1792 x 4096 f16 264 to 268)
     unpack8<T, ECHO_E5M2, false>(s.u, b, s.unpacks);
   }
 }
